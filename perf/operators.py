@@ -12,7 +12,8 @@ run() computes them in plain torch operations, or with `own` set through the lib
 The 4-bit cache: a row of a KV head holds head_dim E2M1 codes (sign, 2 exponent bits, 1 mantissa
 bit: 0, .5, 1, 1.5, 2, 3, 4, 6) and one bf16 scale for each 32 dimensions.  Byte b of the row's
 natural order holds dimension 2b in its low half and 2b + 1 in its high half; the two bytes of
-dimensions 32g + 4r .. 32g + 4r + 3 are stored as the 16-bit unit r * (head_dim / 32) + g.
+dimensions 32g + 4r .. 32g + 4r + 3 are stored as the 16-bit unit r * (head_dim / 32) + g.  With
+head_dim 128, rows 2 and 3 of every four rows of a page hold their two halves swapped.
 """
 import math
 import random
@@ -238,22 +239,29 @@ def _quantize(x):
     return scale, code.flatten(-2)
 
 
+def _swap(b):
+    """Swaps the halves of rows 2 and 3 of every four, where a row is 64 bytes."""
+    if b.shape[-1] != 64:
+        return b
+    odd = torch.arange(b.shape[-2], device=b.device)[:, None] & 2
+    return torch.where(odd > 0, b.roll(32, -1), b)
+
+
 def _pack(code):
-    """Codes [..., d] -> bytes [..., d / 2] in the cache's order."""
+    """Codes [..., page rows, d] -> bytes [..., page rows, d / 2] in the cache's order."""
     b = code[..., 0::2] | (code[..., 1::2] << 4)
-    return b.unflatten(-1, (-1, 8, 2)).transpose(-3, -2).flatten(-3)
+    return _swap(b.unflatten(-1, (-1, 8, 2)).transpose(-3, -2).flatten(-3))
 
 
-def _unpack(b):
-    """Bytes [..., d / 2] -> values of the codes, fp32 [..., d]."""
-    b = b.unflatten(-1, (8, -1, 2)).transpose(-3, -2).flatten(-3).int()
-    c = torch.stack((b & 15, b >> 4), -1).flatten(-2)
-    level = torch.tensor(LEVELS + tuple(-v for v in LEVELS), device=b.device)
-    return level[c]
+def _level(code):
+    return torch.tensor(LEVELS + tuple(-v for v in LEVELS), device=code.device)[code.int()]
 
 
 def _values(codes, scales):
-    return (_unpack(codes).unflatten(-1, (-1, 32)) * scales.float()[..., None]).flatten(-2)
+    """What the rows of whole pages stand for, fp32 [..., page rows, d]."""
+    b = _swap(codes).unflatten(-1, (8, -1, 2)).transpose(-3, -2).flatten(-3)
+    v = _level(torch.stack((b & 15, b >> 4), -1).flatten(-2))
+    return (v.unflatten(-1, (-1, 32)) * scales.float()[..., None]).flatten(-2)
 
 
 def _angles(pos, d):
@@ -377,7 +385,7 @@ def run(s):
         back = {}
         for what in ("k", "v"):
             scale, code = _quantize(s[what].float())
-            back[what] = _values(_pack(code.unflatten(-1, (hkv, d))), scale.unflatten(-1, (hkv, d // 32))).flatten(-2)
+            back[what] = (_level(code).unflatten(-1, (-1, 32)) * scale.float()[..., None]).flatten(-2)
         return {**back, "bias": s["bias"].clone()}
     if own:
         tg.tg_kv4_decode_attention(_cache(s), s["q"], s["tables"], s["lens"], s["gain"], s["temp"], s["ratio"], s["scale"],
@@ -399,12 +407,14 @@ def _near(x):
 
 
 def _row_values(codes, scales):
-    """One page set [..., rows, d / 2] unpacked dimension by dimension, in 64 bits."""
+    """Pages [..., page rows, d / 2] unpacked dimension by dimension, in 64 bits."""
     d = codes.shape[-1] * 2
     dim = torch.arange(d, device=codes.device)
     g, r, j = dim // 32, dim % 32 // 4, dim % 4
     byte = (r * (d // 32) + g) * 2 + j // 2
-    c = codes.index_select(-1, byte).long() >> (4 * (dim % 2)) & 15
+    row = torch.arange(codes.shape[-2], device=codes.device)[:, None]
+    at = torch.where(row % 4 >= 2, byte ^ 32, byte) if d == 128 else byte.expand(row.numel(), d)
+    c = codes.long().gather(-1, at.expand(*codes.shape[:-1], d)) >> (4 * (dim % 2)) & 15
     e, m = c >> 1 & 3, c & 1
     v = torch.where(e > 0, (1 + 0.5 * m) * torch.pow(2.0, (e - 1).double()), 0.5 * m.double())
     return v * (1 - 2 * (c >> 3)).double() * scales.double().index_select(-1, g)
