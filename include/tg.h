@@ -454,13 +454,181 @@ enum { TG_EPI_STORE = 0, TG_EPI_RESIDUAL = 1, TG_EPI_SWIGLU = 2 };
 int tg_linear(const void* x, int64_t ldx, const void* w, void* y, int64_t ldy, int dtype,
               int64_t m, int32_t n_out, int32_t k_in, int epilogue, void* stream);
 
+/*
+ * Page tables of a batch of requests, built on the device from their lengths.
+ * (The TokenGate pages describe one request's cache; holding many requests'
+ * caches in one pool is this library's.)  Request r holds lens[r] rows in
+ * pages of page_rows rows, tables[r][0 .. ceil(lens[r] / page_rows)) naming
+ * them in order; free_pages[0 .. n_free) is a stack of unused page ids.  In
+ * order:
+ *   1. a request with release[r] != 0 returns its pages to the stack (by
+ *      request, then by page) and its length becomes 0;
+ *   2. request r gets new_rows[r] more rows; the pages they need are taken off
+ *      the top of the stack: the i-th page taken, by request and page, is
+ *      free_pages[n_free - 1 - i], entered in the request's table;
+ *   3. slots[t] = page * page_rows + row of the t-th new row (by request),
+ *      row_start[r] = the number of new rows of the requests before r, lengths
+ *      and n_free as they are afterwards.  slots past the last new row are -1.
+ *   lens       device, int32 [nreq];  lens_out device, int32 [nreq] out (may be lens)
+ *   new_rows   device, int32 [nreq];  release device, uint8 [nreq] or NULL (none)
+ *   tables     device, int32 [nreq][max_pages], updated in place (entries past
+ *              a request's pages are left as they are)
+ *   free_pages device, int32 [free_cap], updated in place
+ *   n_free     device, int32 [1];  n_free_out device, int32 [1] out (may be n_free)
+ *   slots      device, int32 [nslots] out;  row_start device, int32 [nreq + 1] out
+ * With lens_out and n_free_out apart from lens and n_free (and no released
+ * request given rows) the call can be repeated with the same result.  A request
+ * that cannot be met (too few pages, a table or slots too short, a negative or
+ * too large length) sets the device error word (TG_ERR_DEVICE_CHECK), and then
+ * nothing changes but slots (all -1) and row_start (all 0).
+ * nreq <= 4096; nreq == 0 only marks the slots.  Errors: TG_ERR_INVALID_ARG (null pointer, sizes < 0,
+ * page_rows or max_pages < 1), TG_ERR_UNSUPPORTED (nreq > 4096).
+ */
+int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                   int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
+                   const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* slots, int32_t nslots,
+                   int32_t* row_start, void* stream);
+
+/*
+ * Per-head RMSNorm of q and k and the rotation to their positions in one pass
+ * ([R] §4.1: RoPE above the gate at the original positions; the step between
+ * the projections and attention in tg_pruned_prefill_layer, for callers that
+ * run it on its own, as a decode step over a paged cache does):
+ *     y = R_pos(x / sqrt(mean(x^2) + norm_eps) * w)     per head row x
+ * with R the rotate-half rotation by pos * rope_theta^(-2i / head_dim).
+ *   q, k     device, dtype, row r of head h at q + r*ldq + h*head_dim (k: hkv heads)
+ *   pos      device, int32 [m] (any sign)
+ *   w_q, w_k device, fp32 [head_dim] or NULL (ones); not read when qk_norm == 0,
+ *            which leaves the norm out
+ *   q_out, k_out  device, dtype, strided rows; may be q and k themselves (with
+ *            the same leading dimension), not overlap them otherwise
+ * fp32 arithmetic, the angle reduced modulo 2 pi in fp64, one rounding to
+ * dtype.  head_dim in {64, 128}; any hq, hkv >= 1; m == 0 does nothing.
+ * Errors: TG_ERR_INVALID_ARG, TG_ERR_UNSUPPORTED (head_dim, m >= 2^31),
+ * TG_ERR_SHAPE (leading dimension below the heads), TG_ERR_ALIGN (rows must be
+ * 16-byte aligned in both dtypes).
+ */
+int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, int64_t m, int32_t hq,
+                    int32_t hkv, int32_t head_dim, const int32_t* pos, const float* w_q, const float* w_k,
+                    int32_t qk_norm, float norm_eps, float rope_theta, void* q_out, int64_t ldqo, void* k_out,
+                    int64_t ldko, void* stream);
+
+/*
+ * Gradients of tg_qk_norm_rope, the step that follows
+ * tg_gated_attention_backward towards the projections.  With g = R_pos^T dy and
+ * r = 1 / sqrt(mean(x^2) + norm_eps):
+ *     dw = sum over rows and heads of g x r,   dx = r g w - x r^3 mean(g w x)
+ *   q .. rope_theta  as the forward's (q, k its inputs)
+ *   dq, dk     device, fp32 [m][heads * head_dim], contiguous: upstream gradients as
+ *              tg_gated_attention_backward writes them
+ *   dq_in, dk_in  device, dtype, strided rows out: gradients of q and k (may be
+ *              q and k themselves: a row is read before it is written)
+ *   dw_q, dw_k device, fp32 [head_dim] out or NULL; zeros when qk_norm == 0
+ *   ws         device workspace of tg_workspace_bytes(TG_OP_QK_ROPE_BWD, 0, m, 0, 0,
+ *              shape) bytes (shape gives head_dim), 16-byte aligned; may be NULL
+ *              when dw_q and dw_k are NULL or qk_norm == 0.  Its contents on
+ *              entry do not matter.
+ * fp32 sums in a fixed order, no atomics: reruns are bit-identical.  m == 0
+ * only zeroes dw_q and dw_k.  Errors: the forward's, TG_ERR_WORKSPACE.
+ */
+int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, int64_t m,
+                             int32_t hq, int32_t hkv, int32_t head_dim, const int32_t* pos, const float* w_q,
+                             const float* w_k, int32_t qk_norm, float norm_eps, float rope_theta, const float* dq,
+                             const float* dk, void* dq_in, int64_t lddq, void* dk_in, int64_t lddk, float* dw_q,
+                             float* dw_k, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The paged gated KV cache in 4 bits.  A row of a KV head is head_dim E2M1 codes
+ * (sign, 2 exponent bits, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6) and a bf16
+ * scale for each 32 dimensions, 4.5 bits a value; the row's key bias (the gate
+ * importance b_c of a kept prompt row, 0 for a generated one) is fp32, one for
+ * all heads.  Caller-owned device memory, 16-byte aligned:
+ *   k_codes, v_codes    uint8 [num_pages][hkv][page_rows][head_dim / 2]
+ *   k_scales, v_scales  bf16  [num_pages][hkv][page_rows][head_dim / 32]
+ *   bias                fp32  [num_pages][page_rows], or NULL (0 for every row)
+ * slot = page * page_rows + row of the page.  In a row, dimensions 32g + 4r .. + 3 are
+ * the 16-bit unit r * (head_dim / 32) + g, first dimension in the low bits; with
+ * head_dim 128, rows 2 and 3 of every four have their two 32-byte halves swapped.
+ * page_rows in {16, 32, 64, 128}, head_dim in {64, 128}, num_pages * page_rows < 2^31.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint16_t* k_scales;
+  uint16_t* v_scales;
+  float* bias;
+  int64_t num_pages;
+  int32_t page_rows;
+  int32_t hkv;
+  int32_t head_dim;
+} tg_kv4_cache;
+
+/*
+ * Rows into the 4-bit cache.  Per group of 32 dimensions: scale = bf16(max|x| / 6),
+ * codes = the nearest E2M1 value of x / scale, ties to the even code, +-6 at most;
+ * both are exact (no input is rounded to the wrong neighbour).  A group with an
+ * infinity or NaN gets scale NaN, so that all its values read back as NaN.
+ *   k, v   device, dtype, row t of KV head g at k + t*ldk + g*head_dim (same for v / ldv)
+ *   bias   device fp32 [rows] or NULL (0); ignored when the cache has none
+ *   slots  device int32 [rows]: where each row goes (tg_page_tables' slots); a
+ *          negative slot leaves its row out.  A slot past the cache sets the device error
+ *          word and is left out.  With a slot given twice it is unspecified which
+ *          row's groups stay.
+ * rows == 0 does nothing.  Errors: TG_ERR_INVALID_ARG (null pointer, rows < 0,
+ * page_rows, hkv, num_pages, dtype), TG_ERR_UNSUPPORTED (head_dim, 2^31 slots or rows),
+ * TG_ERR_SHAPE (leading dimension), TG_ERR_ALIGN.
+ */
+int tg_kv4_store(const tg_kv4_cache* cache, const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
+                 int64_t rows, const float* bias, const int32_t* slots, void* stream);
+
+/*
+ * Rows out of the 4-bit cache: the values the codes stand for, code * scale,
+ * rounded once to dtype (exact in fp32).  Rows with a negative slot are left as
+ * they are.  bias (out) may be NULL.  Arguments and errors as tg_kv4_store.
+ */
+int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, void* k, int64_t ldk, void* v,
+                int64_t ldv, int dtype, float* bias, void* stream);
+
+/*
+ * One decode step of token-gated attention for a batch of requests over the
+ * paged 4-bit cache: tg_gated_decode_attention per request, with the keys and
+ * values the 4-bit rows stand for.  For request r, query head h of KV head
+ * g = h / (hq / hkv), and its rows c < lens[r]:
+ *     l_c = head_temp[h] * ratio[r] * sm_scale * (q_h . k_c) + head_gain[h] * bias[c]
+ *     out_h = sum_c softmax_c(l) v_c,   lse_h = log sum_c exp(l_c)
+ * A key whose bias is -infinity is left out, whatever its row holds (head_gain > 0).
+ * A request with no row left gets zeros and lse -infinity.
+ *   q      device, dtype, request r's head h at q + r*ldq + h*head_dim
+ *   tables device int32 [nreq][max_pages], lens device int32 [nreq] (as
+ *          tg_page_tables leaves them; the new token's row is among the lens[r] rows)
+ *   head_gain, head_temp  device fp32 [hq];  ratio device fp32 [nreq] or NULL (1)
+ *   out    device, dtype, rows as q;  lse device fp32 [nreq][hq] or NULL
+ *   ws     device workspace of tg_workspace_bytes(TG_OP_KV4_DECODE, 0, 0, 0, 0, shape)
+ *          bytes (shape gives hq, hkv, head_dim), 16-byte aligned; the size depends on
+ *          the SM count, not on the batch
+ *   flags  0, or TG_WS_KEPT_ZERO: ws is zero-filled or as the previous successful
+ *          call with this flag left it, and the call launches no memset
+ * bf16 or fp32 queries; head_dim in {64, 128}; at most 8 query heads per KV head; nreq
+ * <= 4096; nreq == 0 does nothing.  A length that is negative or beyond the table
+ * counts as 0, a page id outside the cache as page 0, and either sets the device error word.
+ * The lengths are read on the device, so a captured call follows them.
+ * Errors: TG_ERR_INVALID_ARG, TG_ERR_UNSUPPORTED, TG_ERR_SHAPE, TG_ERR_ALIGN (q and
+ * out rows 16-byte aligned), TG_ERR_WORKSPACE.
+ */
+int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ldq, int dtype,
+                            const int32_t* tables, int32_t max_pages, const int32_t* lens, int32_t nreq, int32_t hq,
+                            const float* head_gain, const float* head_temp, const float* ratio, float sm_scale,
+                            void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes, uint32_t flags,
+                            void* stream);
+
 enum { TG_OP_GATE_SCORE = 0, TG_OP_LAYER = 1, TG_OP_ATTENTION = 2, TG_OP_DECODE = 3, TG_OP_ATTENTION_BWD = 4,
-       TG_OP_GATE_SELECT = 5 };
+       TG_OP_GATE_SELECT = 5, TG_OP_QK_ROPE_BWD = 6, TG_OP_KV4_DECODE = 7 };
 
 /* Workspace bytes needed by an op: TG_OP_GATE_SCORE and TG_OP_GATE_SELECT use n, d_model and h;
  * TG_OP_LAYER and TG_OP_ATTENTION use m and shape (TG_OP_ATTENTION reads its
  * dtype, hq, hkv and head_dim); TG_OP_DECODE uses m = the cache length and
- * shape's hq, hkv and head_dim; TG_OP_ATTENTION_BWD uses m and shape's hq, hkv and head_dim.  Returns 0 for an invalid request, and 0 for
+ * shape's hq, hkv and head_dim; TG_OP_ATTENTION_BWD uses m and shape's hq, hkv and head_dim;
+ * TG_OP_QK_ROPE_BWD uses m and shape's head_dim; TG_OP_KV4_DECODE uses shape's hq, hkv and head_dim.  Returns 0 for an invalid request, and 0 for
  * TG_OP_ATTENTION when the attention needs no workspace. */
 size_t tg_workspace_bytes(int op, int64_t n, int64_t m, int32_t d_model, int32_t h, const tg_layer_shape* shape);
 

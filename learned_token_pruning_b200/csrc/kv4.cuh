@@ -1,0 +1,386 @@
+// The paged 4-bit KV cache: page tables and slot maps built on the device, and
+// rows moved in and out of the cache.
+//
+// A cache row of one KV head is D E2M1 codes (sign, 2 exponent bits, 1 mantissa
+// bit: the values 0, .5, 1, 1.5, 2, 3, 4, 6) and one bf16 scale per 32
+// dimensions: 4.5 bits a value.  Layout of a page (kv4 cache in tg.h):
+//   codes  [page][head][row][D / 2] bytes,  scales [page][head][row][D / 32] bf16
+// so that one head's rows of a page are one contiguous block, which a bulk copy
+// takes as it is.  Inside a row the 16-bit unit of dimensions 32g + 4r .. + 3
+// (low nibble first) sits at unit r * (D / 32) + g: the four units a decode lane
+// needs, one per scale group, are neighbours.  At D = 128 a row is 64 bytes, and
+// rows 2 and 3 of every four hold their 32-byte halves swapped, so that a warp
+// reading 8 bytes of each of four neighbouring rows meets every bank once.
+#pragma once
+
+#include "common.cuh"
+
+namespace tg {
+
+// consistency checks of the paged cache (device error word, see common.cuh)
+constexpr uint32_t kErrPageTable = 4;  // lengths, new rows, tables or the free list do not fit
+constexpr uint32_t kErrKvSlot = 5;     // slot past the cache
+constexpr uint32_t kErrKvPage = 6;     // page id or request length out of range
+
+struct Kv4Cache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  __nv_bfloat16* k_scales;
+  __nv_bfloat16* v_scales;
+  float* bias;        // [num_pages][page_rows] or null
+  int64_t num_pages;
+  int32_t page_rows;  // 16, 32, 64 or 128
+  int32_t page_shift;
+  int32_t hkv;
+};
+
+// index of the (page, head, row) triple of a slot
+__device__ __forceinline__ int64_t kv4_row(const Kv4Cache& c, int32_t slot, int head) {
+  const int64_t page = slot >> c.page_shift;
+  return ((page * c.hkv + head) << c.page_shift) + (slot & (c.page_rows - 1));
+}
+
+// ---------------------------------------------------------------------------
+// Page tables.  One cluster of CTAs: each scans all requests by itself (three
+// prefix sums in shared memory: returned pages, taken pages, new rows) and then
+// takes its share of the page moves and of the slots.  The cluster barriers
+// order the reads of the old state before the writes of the new one, so the
+// state may be updated in place.  Bound by latency: the two barriers and the
+// dependent loads (length -> page -> slot).
+// ---------------------------------------------------------------------------
+constexpr int kTabThreads = 512;
+constexpr int kTabMaxReq = 4096;
+constexpr int kTabPer = kTabMaxReq / kTabThreads;  // requests per thread at most
+
+struct PageTableParams {
+  const int32_t* lens;
+  const int32_t* new_rows;
+  const uint8_t* release;  // or null
+  int32_t nreq;
+  int32_t page_rows;
+  int32_t* tables;
+  int32_t max_pages;
+  int32_t* free_pages;
+  int32_t free_cap;
+  const int32_t* n_free;
+  int32_t* lens_out;
+  int32_t* n_free_out;
+  int32_t* slots;
+  int32_t nslots;
+  int32_t* row_start;
+};
+
+__host__ __device__ constexpr size_t page_table_smem(int nreq) { return static_cast<size_t>(4 * nreq + 3) * 4; }
+
+// largest r with start[r] <= i (start ascending, start[0] = 0, i < start[n]); the
+// requests without items have start[r] == start[r + 1] and are never returned
+__device__ __forceinline__ int find_request(const int32_t* start, int n, int32_t i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void block_scan3(int64_t (&v)[3], int64_t (*s_warp)[3], int64_t (&before)[3],
+                                            int64_t (&total)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    inc[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc[k], o);
+      if (lane >= o) inc[k] += up;
+    }
+    if (lane == 31) s_warp[warp][k] = inc[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int64_t base = 0, all = 0;
+    for (int w = 0; w < kTabThreads / 32; ++w) {
+      if (w < warp) base += s_warp[w][k];
+      all += s_warp[w][k];
+    }
+    before[k] = base + inc[k] - v[k];
+    total[k] = all;
+  }
+}
+
+__global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTableParams p) {
+  extern __shared__ int32_t s_tab[];
+  __shared__ int64_t s_warp[kTabThreads / 32][3];
+  __shared__ int s_bad;
+  int32_t* s_len = s_tab;                   // [nreq] rows held before this call's new ones
+  int32_t* s_back = s_len + p.nreq;         // [nreq + 1] first returned page
+  int32_t* s_take = s_back + p.nreq + 1;    // [nreq + 1] first taken page
+  int32_t* s_rows = s_take + p.nreq + 1;    // [nreq + 1] first new row
+  const int rank = static_cast<int>(cluster_ctarank()), size = static_cast<int>(gridDim.x);
+  if (threadIdx.x == 0) s_bad = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int64_t P = p.page_rows, most = static_cast<int64_t>(p.max_pages) * P;
+  const int per = (p.nreq + kTabThreads - 1) / kTabThreads;
+  const int r0 = threadIdx.x * per;
+  int32_t len[kTabPer], add[kTabPer], back[kTabPer], take[kTabPer];
+  int64_t v[3] = {0, 0, 0};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kTabPer; ++i) {
+    len[i] = add[i] = back[i] = take[i] = 0;
+    const int r = r0 + i;
+    if (i < per && r < p.nreq) {
+      int64_t l = p.lens[r];
+      const int64_t n = p.new_rows[r];
+      if (l < 0 || l > most || n < 0) bad = true;
+      else {
+        if (p.release && p.release[r]) {
+          back[i] = static_cast<int32_t>((l + P - 1) / P);
+          l = 0;
+        }
+        if (l + n > most) bad = true;
+        else {
+          len[i] = static_cast<int32_t>(l);
+          add[i] = static_cast<int32_t>(n);
+          take[i] = static_cast<int32_t>((l + n + P - 1) / P - (l + P - 1) / P);
+        }
+      }
+    }
+    v[0] += back[i];
+    v[1] += take[i];
+    v[2] += add[i];
+  }
+  if (bad) s_bad = 1;  // same value from every writer
+  int64_t before[3], total[3];
+  block_scan3(v, s_warp, before, total);  // its barrier also publishes s_bad
+  const int64_t nf = *p.n_free;
+  // one verdict from the same inputs in every CTA
+  const bool refuse = s_bad || nf < 0 || nf + total[0] > p.free_cap || total[1] > nf + total[0] || total[2] > p.nslots;
+#pragma unroll
+  for (int i = 0; i < kTabPer; ++i) {
+    const int r = r0 + i;
+    if (i < per && r < p.nreq) {
+      s_len[r] = len[i];
+      s_back[r] = static_cast<int32_t>(before[0]);
+      s_take[r] = static_cast<int32_t>(before[1]);
+      s_rows[r] = static_cast<int32_t>(before[2]);
+    }
+    before[0] += back[i];
+    before[1] += take[i];
+    before[2] += add[i];
+  }
+  if (threadIdx.x == 0) {
+    s_back[p.nreq] = static_cast<int32_t>(total[0]);
+    s_take[p.nreq] = static_cast<int32_t>(total[1]);
+    s_rows[p.nreq] = static_cast<int32_t>(total[2]);
+  }
+  __syncthreads();
+  cluster_sync_all();  // every CTA has read the old lengths and free count
+  const int t0 = rank * kTabThreads + threadIdx.x, step = size * kTabThreads;
+  if (refuse) {
+    if (t0 == 0) raise_error(kErrPageTable, s_bad ? 1u : (total[1] > nf + total[0] ? 2u : 3u));
+    for (int i = t0; i < p.nslots; i += step) p.slots[i] = -1;
+    for (int i = t0; i <= p.nreq; i += step) p.row_start[i] = 0;
+    for (int i = t0; i < p.nreq && p.lens_out != p.lens; i += step) p.lens_out[i] = p.lens[i];
+    if (t0 == 0) *p.n_free_out = static_cast<int32_t>(nf);
+    return;
+  }
+  const int32_t nback = static_cast<int32_t>(total[0]), ntake = static_cast<int32_t>(total[1]);
+  const int32_t nrows = static_cast<int32_t>(total[2]), top = static_cast<int32_t>(nf + total[0]);
+  for (int i = t0; i < nback; i += step) {
+    const int r = find_request(s_back, p.nreq, i);
+    p.free_pages[nf + i] = p.tables[static_cast<int64_t>(r) * p.max_pages + (i - s_back[r])];
+  }
+  if (nback) cluster_sync_all();  // returned pages are listed before any page is taken
+  for (int i = t0; i < ntake; i += step) {
+    const int r = find_request(s_take, p.nreq, i);
+    const int first = (s_len[r] + p.page_rows - 1) / p.page_rows;
+    p.tables[static_cast<int64_t>(r) * p.max_pages + first + (i - s_take[r])] = __ldcg(p.free_pages + (top - 1 - i));
+  }
+  for (int i = t0; i < p.nslots; i += step) {
+    int32_t slot = -1;
+    if (i < nrows) {
+      const int r = find_request(s_rows, p.nreq, i);
+      const int32_t at = s_len[r] + (i - s_rows[r]);
+      const int32_t page = at / p.page_rows, held = (s_len[r] + p.page_rows - 1) / p.page_rows;
+      // pages taken in this call are read off the free list (another thread writes the table)
+      const int32_t id = page < held ? p.tables[static_cast<int64_t>(r) * p.max_pages + page]
+                                     : __ldcg(p.free_pages + (top - 1 - (s_take[r] + page - held)));
+      if (id < 0) raise_error(kErrPageTable, 4);
+      else slot = id * p.page_rows + (at - page * p.page_rows);
+    }
+    p.slots[i] = slot;
+  }
+  for (int i = t0; i <= p.nreq; i += step) {
+    p.row_start[i] = s_rows[i];
+    if (i < p.nreq) p.lens_out[i] = s_len[i] + (s_rows[i + 1] - s_rows[i]);
+  }
+  if (t0 == 0) *p.n_free_out = top - ntake;
+}
+
+// ---------------------------------------------------------------------------
+// Rows in and out.  Four lanes share a group of 32 dimensions, eight dimensions
+// (one 16-byte load in bf16) each.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(ww[i]);
+    x[2 * i + 1] = bf16_hi(ww[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]);
+template <>
+__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                            pack_bf16x2(x[6], x[7]));
+}
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Nearest E2M1 code of x / s for s > 0, ties to the even code, by comparing |x|
+// with the seven borders times s.  A border has at most 3 significant bits and s
+// is bf16, so the products are exact and the code is the exact nearest one.
+__device__ __forceinline__ uint32_t e2m1_code(float x, float s) {
+  const float a = fabsf(x);
+  uint32_t c = 0;
+  c += a > 0.25f * s;
+  c += a >= 0.75f * s;
+  c += a > 1.25f * s;
+  c += a >= 1.75f * s;
+  c += a > 2.5f * s;
+  c += a >= 3.5f * s;
+  c += a > 5.0f * s;
+  return c | (__float_as_uint(x) >> 28 & 8u);
+}
+
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t e = c >> 1 & 3u, m = c & 1u;
+  const float v = e ? __uint_as_float((126u + e) << 23 | m << 22) : 0.5f * static_cast<float>(m);
+  return c & 8u ? -v : v;
+}
+
+struct Kv4RowsParams {
+  Kv4Cache c;
+  const void* k;   // rows in (store) or out (load)
+  const void* v;
+  int64_t ldk, ldv;
+  float* bias;     // row biases in (store) or out (load), or null
+  const int32_t* slots;
+  int64_t rows;
+};
+
+// byte offset in a row of the 32-bit word that holds units (r, 2gp) and (r, 2gp + 1)
+template <int D>
+__device__ __forceinline__ int kv4_word(int r, int gp, int32_t slot) {
+  const int at = (r * (D / 64) + gp) * 4;
+  return D == 128 ? at ^ ((slot & 2) << 4) : at;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_kv4_store(const Kv4RowsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int L = D / 8;  // lanes per head row
+  const int per_row = 2 * p.c.hkv * L;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = i / per_row;
+  const bool in = row < p.rows;  // uniform over the eight lanes a shuffle reaches
+  const int li = static_cast<int>(i - row * per_row);
+  const int head2 = li / L, l = li % L, g = l >> 2, l4 = l & 3;
+  const bool is_v = head2 >= p.c.hkv;
+  const int head = is_v ? head2 - p.c.hkv : head2;
+  int32_t slot = in ? p.slots[row] : -1;
+  if (slot >= 0 && slot >= p.c.num_pages * p.c.page_rows) {
+    if (li == 0) raise_error(kErrKvSlot, 1);
+    slot = -1;
+  }
+  float x[8] = {};
+  if (slot >= 0)
+    load8(static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ldv : p.ldk) + head * D + l * 8, x);
+  // largest magnitude of the group as an integer: infinities and NaN come out on top
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // max / 6 in fp32, rounded to bf16: the second rounding meets no false tie
+  // (a quotient by 6 that is not a bf16 tie stays an fp32 step away from one)
+  const bool finite = top < 0x7f800000u;
+  const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? __uint_as_float(top) / 6.0f : __uint_as_float(0x7fffffffu));
+  const float s = __bfloat162float(sb);
+  uint32_t w = 0;  // eight codes, dimension 8l first
+  if (finite && s > 0.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= e2m1_code(x[e], s) << (4 * e);
+  }
+  // low half: unit (2 l4, g); high half: (2 l4 + 1, g).  The lane of the neighbouring
+  // group has the same units of group g ^ 1: each keeps one and hands over the other.
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, g & 1 ? w & 0xffffu : w >> 16, 4);
+  const uint32_t word = g & 1 ? got | (w & 0xffff0000u) : (w & 0xffffu) | got << 16;
+  if (slot < 0) return;
+  const int64_t at = kv4_row(p.c, slot, head);
+  const int r = 2 * l4 + (g & 1), gp = g >> 1;
+  uint8_t* codes = (is_v ? p.c.v_codes : p.c.k_codes) + at * (D / 2);
+  *reinterpret_cast<uint32_t*>(codes + kv4_word<D>(r, gp, slot)) = word;
+  if (l4 == 0) (is_v ? p.c.v_scales : p.c.k_scales)[at * (D / 32) + g] = sb;
+  if (li == 0 && p.c.bias) p.c.bias[slot] = p.bias ? p.bias[row] : 0.0f;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_kv4_load(const Kv4RowsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int L = D / 8;
+  const int per_row = 2 * p.c.hkv * L;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = i / per_row;
+  const bool in = row < p.rows;
+  const int li = static_cast<int>(i - row * per_row);
+  const int head2 = li / L, l = li % L, g = l >> 2, l4 = l & 3;
+  const bool is_v = head2 >= p.c.hkv;
+  const int head = is_v ? head2 - p.c.hkv : head2;
+  int32_t slot = in ? p.slots[row] : -1;
+  if (slot >= 0 && slot >= p.c.num_pages * p.c.page_rows) {
+    if (li == 0) raise_error(kErrKvSlot, 2);
+    slot = -1;
+  }
+  const int64_t at = slot >= 0 ? kv4_row(p.c, slot, head) : 0;
+  const int r = 2 * l4 + (g & 1), gp = g >> 1;
+  uint32_t word = 0;
+  float s = 0.0f;
+  if (slot >= 0) {
+    word = *reinterpret_cast<const uint32_t*>((is_v ? p.c.v_codes : p.c.k_codes) + at * (D / 2) + kv4_word<D>(r, gp, slot));
+    s = __bfloat162float((is_v ? p.c.v_scales : p.c.k_scales)[at * (D / 32) + g]);
+  }
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, g & 1 ? word & 0xffffu : word >> 16, 4);
+  const uint32_t w = g & 1 ? got | (word & 0xffff0000u) : (word & 0xffffu) | got << 16;
+  if (slot < 0) return;
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = e2m1_value(w >> (4 * e) & 15u) * s;
+  store8(static_cast<T*>(const_cast<void*>(is_v ? p.v : p.k)) + row * (is_v ? p.ldv : p.ldk) + head * D + l * 8, x);
+  if (li == 0 && p.bias) p.bias[row] = p.c.bias ? p.c.bias[slot] : 0.0f;
+}
+
+}  // namespace tg

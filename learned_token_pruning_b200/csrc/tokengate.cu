@@ -29,6 +29,9 @@
 #include "decode.cuh"
 #include "gather.cuh"
 #include "gemm_tc.cuh"
+#include "kv4.cuh"
+#include "kv4_decode.cuh"
+#include "qk_rope.cuh"
 #include "select.cuh"
 #include "simt.cuh"
 
@@ -505,6 +508,9 @@ static int topk_select_impl(const float* scores, const uint8_t* prunable, int64_
                             int32_t* kept_idx, int64_t m, const uint32_t* hist_top, void* stream,
                             uint32_t* hist_clear = nullptr);
 
+static size_t qk_rope_bwd_ws_bytes(int64_t m, int head_dim);
+static size_t kv4_decode_ws_bytes(int group, int head_dim);
+
 extern "C" {
 
 const char* tg_version(void) { return TG_VERSION; }
@@ -739,6 +745,16 @@ size_t tg_workspace_bytes(int op, int64_t n, int64_t m, int32_t d_model, int32_t
   if (op == TG_OP_DECODE) {
     if (!shape || m <= 0 || shape->hkv <= 0 || shape->hq % shape->hkv) return 0;
     return decode_ws_bytes(m, shape->hkv, shape->hq / shape->hkv, shape->head_dim);
+  }
+  if (op == TG_OP_QK_ROPE_BWD) {
+    if (!shape || m <= 0 || (shape->head_dim != 64 && shape->head_dim != 128)) return 0;
+    return qk_rope_bwd_ws_bytes(m, shape->head_dim);
+  }
+  if (op == TG_OP_KV4_DECODE) {
+    if (!shape || shape->hkv <= 0 || shape->hq <= 0 || shape->hq % shape->hkv ||
+        shape->hq / shape->hkv > tg::kKv4MaxGroup || (shape->head_dim != 64 && shape->head_dim != 128))
+      return 0;
+    return kv4_decode_ws_bytes(shape->hq / shape->hkv, shape->head_dim);
   }
   return 0;
 }
@@ -1716,5 +1732,335 @@ int tg_gate_score_noalloc(const void* hidden, int dtype, int64_t n, int32_t d_mo
 }
 
 size_t tg_gate_score_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Per-head norm and rotation of q and k on its own, and its gradients
+// ---------------------------------------------------------------------------
+namespace {
+
+// Frequencies theta^(-2i/D), kept per host thread while theta and D stay the same.
+const tg::RopeTable& rope_table(float theta, int head_dim) {
+  thread_local tg::RopeTable tab{};
+  thread_local float last_theta = 0.0f;
+  thread_local int last_dim = 0;
+  if (theta != last_theta || head_dim != last_dim) {
+    for (int i = 0; i < head_dim / 2; ++i) tab.inv_freq[i] = std::pow(static_cast<double>(theta), -2.0 * i / head_dim);
+    last_theta = theta;
+    last_dim = head_dim;
+  }
+  return tab;
+}
+
+int check_strided(const char* name, const void* p, int64_t ld, int64_t width, int es) {
+  if (!p) return fail(TG_ERR_INVALID_ARG, "%s is null", name);
+  if (ld < width) return fail(TG_ERR_SHAPE, "%s: leading dimension smaller than the heads it holds", name);
+  if (!aligned16(p) || (ld * es) % 16) return fail(TG_ERR_ALIGN, "%s: rows need 16-byte alignment", name);
+  return TG_OK;
+}
+
+int check_qk(int dtype, int64_t m, int32_t hq, int32_t hkv, int32_t head_dim, float norm_eps, float rope_theta) {
+  if (m < 0 || hq <= 0 || hkv <= 0) return fail(TG_ERR_INVALID_ARG, "bad m / heads");
+  if (!dtype_size(dtype)) return fail(TG_ERR_INVALID_ARG, "dtype");
+  if (!(norm_eps >= 0.0f) || !(rope_theta > 0.0f) || std::isinf(rope_theta))
+    return fail(TG_ERR_INVALID_ARG, "norm_eps must be >= 0 and rope_theta positive and finite");
+  if (head_dim != 64 && head_dim != 128) return fail(TG_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (m >= (int64_t(1) << 31) || hq > 65536 || hkv > 65536) return fail(TG_ERR_UNSUPPORTED, "m must be < 2^31, heads <= 65536");
+  return TG_OK;
+}
+
+int qk_rope_bwd_blocks(int64_t m) {
+  return static_cast<int>(std::min<int64_t>((m + tg::kRopeWarps - 1) / tg::kRopeWarps, 2 * sm_count()));
+}
+
+}  // namespace
+
+static size_t qk_rope_bwd_ws_bytes(int64_t m, int head_dim) {
+  return static_cast<size_t>(qk_rope_bwd_blocks(m)) * 2 * head_dim * sizeof(float);
+}
+
+extern "C" {
+
+int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, int64_t m, int32_t hq,
+                    int32_t hkv, int32_t head_dim, const int32_t* pos, const float* w_q, const float* w_k,
+                    int32_t qk_norm, float norm_eps, float rope_theta, void* q_out, int64_t ldqo, void* k_out,
+                    int64_t ldko, void* stream) {
+  int rc = check_qk(dtype, m, hq, hkv, head_dim, norm_eps, rope_theta);
+  if (rc) return rc;
+  if (m == 0) return TG_OK;
+  const int es = dtype_size(dtype);
+  const int64_t wq = int64_t(hq) * head_dim, wk = int64_t(hkv) * head_dim;
+  if ((rc = check_strided("q", q, ldq, wq, es)) || (rc = check_strided("k", k, ldk, wk, es)) ||
+      (rc = check_strided("q_out", q_out, ldqo, wq, es)) || (rc = check_strided("k_out", k_out, ldko, wk, es)))
+    return rc;
+  if (!pos) return fail(TG_ERR_INVALID_ARG, "pos is null");
+  if ((q == q_out && ldq != ldqo) || (k == k_out && ldk != ldko))
+    return fail(TG_ERR_SHAPE, "in place needs the same leading dimension");
+  tg::QkRopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.m = m;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.pos = pos;
+  p.wq = w_q;
+  p.wk = w_k;
+  p.qk_norm = qk_norm;
+  p.eps = norm_eps;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.ldqo = ldqo;
+  p.ldko = ldko;
+  p.split = 1;
+  const dim3 grid(static_cast<unsigned>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps)), block(32 * tg::kRopeWarps);
+  const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
+  cudaStream_t st = as_stream(stream);
+  auto run = [&](auto kern) { return launch_pdl("k_qk_rope_fwd", kern, grid, block, 0, st, p, tab); };
+  if (dtype == TG_BF16)
+    return head_dim == 128 ? run(tg::k_qk_rope_fwd<__nv_bfloat16, 128>) : run(tg::k_qk_rope_fwd<__nv_bfloat16, 64>);
+  return head_dim == 128 ? run(tg::k_qk_rope_fwd<float, 128>) : run(tg::k_qk_rope_fwd<float, 64>);
+}
+
+int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t ldk, int dtype, int64_t m,
+                             int32_t hq, int32_t hkv, int32_t head_dim, const int32_t* pos, const float* w_q,
+                             const float* w_k, int32_t qk_norm, float norm_eps, float rope_theta, const float* dq,
+                             const float* dk, void* dq_in, int64_t lddq, void* dk_in, int64_t lddk, float* dw_q,
+                             float* dw_k, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_qk(dtype, m, hq, hkv, head_dim, norm_eps, rope_theta);
+  if (rc) return rc;
+  cudaStream_t st = as_stream(stream);
+  const int es = dtype_size(dtype);
+  const bool sums = (dw_q || dw_k) && qk_norm && m > 0;
+  if (m > 0) {
+    const int64_t wq = int64_t(hq) * head_dim, wk = int64_t(hkv) * head_dim;
+    if ((rc = check_strided("q", q, ldq, wq, es)) || (rc = check_strided("k", k, ldk, wk, es)) ||
+        (rc = check_strided("dq_in", dq_in, lddq, wq, es)) || (rc = check_strided("dk_in", dk_in, lddk, wk, es)))
+      return rc;
+    if (!pos || !dq || !dk) return fail(TG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(dq) || !aligned16(dk)) return fail(TG_ERR_ALIGN, "dq and dk must be 16-byte aligned");
+    if ((q == dq_in && ldq != lddq) || (k == dk_in && ldk != lddk))
+      return fail(TG_ERR_SHAPE, "in place needs the same leading dimension");
+    if (sums) {
+      const size_t need = qk_rope_bwd_ws_bytes(m, head_dim);
+      if (!ws || ws_bytes < need) return fail(TG_ERR_WORKSPACE, "q/k norm gradients need %zu workspace bytes", need);
+      if (!aligned16(ws)) return fail(TG_ERR_ALIGN, "workspace must be 16-byte aligned");
+    }
+  }
+  if (!sums)
+    for (float* dw : {dw_q, dw_k})
+      if (dw && cudaMemsetAsync(dw, 0, head_dim * sizeof(float), st) != cudaSuccess)
+        return fail(TG_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(cudaGetLastError()));
+  if (m == 0) return TG_OK;
+  tg::QkRopeParams p{};
+  p.q = q;
+  p.k = k;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.m = m;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.pos = pos;
+  p.wq = w_q;
+  p.wk = w_k;
+  p.qk_norm = qk_norm;
+  p.eps = norm_eps;
+  p.q_out = dq_in;
+  p.k_out = dk_in;
+  p.ldqo = lddq;
+  p.ldko = lddk;
+  p.dq = dq;
+  p.dk = dk;
+  p.part = sums ? static_cast<float*>(ws) : nullptr;
+  const int blocks = qk_rope_bwd_blocks(m);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(32 * tg::kRopeWarps);
+  const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
+  auto run = [&](auto kern) { return launch_pdl("k_qk_rope_bwd", kern, grid, block, 0, st, p, tab); };
+  if (dtype == TG_BF16)
+    rc = head_dim == 128 ? run(tg::k_qk_rope_bwd<__nv_bfloat16, 128>) : run(tg::k_qk_rope_bwd<__nv_bfloat16, 64>);
+  else
+    rc = head_dim == 128 ? run(tg::k_qk_rope_bwd<float, 128>) : run(tg::k_qk_rope_bwd<float, 64>);
+  if (rc || !sums) return rc;
+  return launch_pdl("k_qk_rope_bwd_final", tg::k_qk_rope_bwd_final, dim3(2), dim3(4 * head_dim), 0, st,
+                    static_cast<const float*>(p.part), blocks, int(head_dim), dw_q, dw_k);
+}
+
+// ---------------------------------------------------------------------------
+// The paged 4-bit cache
+// ---------------------------------------------------------------------------
+int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                   int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
+                   const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* slots, int32_t nslots,
+                   int32_t* row_start, void* stream) {
+  if (nreq < 0 || nslots < 0 || free_cap < 0 || page_rows < 1 || max_pages < 1)
+    return fail(TG_ERR_INVALID_ARG, "bad sizes");
+  if (!n_free || !n_free_out || !row_start || (nslots > 0 && !slots) || (free_cap > 0 && !free_pages))
+    return fail(TG_ERR_INVALID_ARG, "null pointer");
+  if (nreq > 0 && (!lens || !new_rows || !tables || !lens_out)) return fail(TG_ERR_INVALID_ARG, "null pointer");
+  if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
+  if (int64_t(max_pages) * page_rows >= (int64_t(1) << 31))
+    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
+  tg::PageTableParams p{};
+  p.lens = lens;
+  p.new_rows = new_rows;
+  p.release = release;
+  p.nreq = nreq;
+  p.page_rows = page_rows;
+  p.tables = tables;
+  p.max_pages = max_pages;
+  p.free_pages = free_pages;
+  p.free_cap = free_cap;
+  p.n_free = n_free;
+  p.lens_out = lens_out;
+  p.n_free_out = n_free_out;
+  p.slots = slots;
+  p.nslots = nslots;
+  p.row_start = row_start;
+  const size_t smem = tg::page_table_smem(nreq);
+  int rc = set_smem(tg::k_page_tables, tg::page_table_smem(tg::kTabMaxReq));
+  if (rc) return rc;
+  const unsigned size = int64_t(nslots) + nreq <= 4 * tg::kTabThreads ? 1 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(tg::kTabThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = as_stream(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tg::k_page_tables, p);
+  if (e != cudaSuccess) return fail(TG_ERR_CUDA, "k_page_tables launch: %s", cudaGetErrorString(e));
+  return check_launch("k_page_tables");
+}
+
+}  // extern "C"
+
+namespace {
+
+int kv4_cache(const tg_kv4_cache* c, tg::Kv4Cache* out) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return fail(TG_ERR_INVALID_ARG, "null cache pointer");
+  if (c->num_pages <= 0 || c->hkv <= 0 || c->hkv > 65536) return fail(TG_ERR_INVALID_ARG, "bad num_pages / hkv");
+  if (c->page_rows != 16 && c->page_rows != 32 && c->page_rows != 64 && c->page_rows != 128)
+    return fail(TG_ERR_INVALID_ARG, "page_rows must be 16, 32, 64 or 128");
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(TG_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (c->num_pages >= (int64_t(1) << 31) / c->page_rows) return fail(TG_ERR_UNSUPPORTED, "the cache must have < 2^31 slots");
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales) ||
+      !aligned16(c->bias))
+    return fail(TG_ERR_ALIGN, "cache pools must be 16-byte aligned");
+  out->k_codes = c->k_codes;
+  out->v_codes = c->v_codes;
+  out->k_scales = reinterpret_cast<__nv_bfloat16*>(c->k_scales);
+  out->v_scales = reinterpret_cast<__nv_bfloat16*>(c->v_scales);
+  out->bias = c->bias;
+  out->num_pages = c->num_pages;
+  out->page_rows = c->page_rows;
+  out->page_shift = c->page_rows == 16 ? 4 : c->page_rows == 32 ? 5 : c->page_rows == 64 ? 6 : 7;
+  out->hkv = c->hkv;
+  return TG_OK;
+}
+
+int kv4_rows(const char* what, bool load, const tg_kv4_cache* cache, const void* k, int64_t ldk, const void* v,
+             int64_t ldv, int dtype, int64_t rows, const float* bias, const int32_t* slots, cudaStream_t st) {
+  tg::Kv4RowsParams p{};
+  int rc = kv4_cache(cache, &p.c);
+  if (rc) return rc;
+  const int es = dtype_size(dtype);
+  if (!es) return fail(TG_ERR_INVALID_ARG, "dtype");
+  if (rows < 0) return fail(TG_ERR_INVALID_ARG, "rows must be >= 0");
+  if (rows == 0) return TG_OK;
+  const int64_t width = int64_t(cache->hkv) * cache->head_dim;
+  if ((rc = check_strided("k", k, ldk, width, es)) || (rc = check_strided("v", v, ldv, width, es))) return rc;
+  if (!slots) return fail(TG_ERR_INVALID_ARG, "slots is null");
+  const int64_t blocks = (rows * (width / 4) + 255) / 256;  // one thread per eight K or V values
+  if (rows >= (int64_t(1) << 31) || blocks >= (int64_t(1) << 31)) return fail(TG_ERR_UNSUPPORTED, "too many rows");
+  p.k = k;
+  p.v = v;
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.bias = const_cast<float*>(bias);
+  p.slots = slots;
+  p.rows = rows;
+  auto run = [&](auto kern) { return launch_pdl(what, kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p); };
+  const bool bf = dtype == TG_BF16, wide = cache->head_dim == 128;
+  if (load)
+    return bf ? (wide ? run(tg::k_kv4_load<__nv_bfloat16, 128>) : run(tg::k_kv4_load<__nv_bfloat16, 64>))
+              : (wide ? run(tg::k_kv4_load<float, 128>) : run(tg::k_kv4_load<float, 64>));
+  return bf ? (wide ? run(tg::k_kv4_store<__nv_bfloat16, 128>) : run(tg::k_kv4_store<__nv_bfloat16, 64>))
+            : (wide ? run(tg::k_kv4_store<float, 128>) : run(tg::k_kv4_store<float, 64>));
+}
+
+}  // namespace
+
+static size_t kv4_decode_ws_bytes(int group, int head_dim) {
+  return static_cast<size_t>(group) * head_dim;
+}
+
+extern "C" {
+
+int tg_kv4_store(const tg_kv4_cache* cache, const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
+                 int64_t rows, const float* bias, const int32_t* slots, void* stream) {
+  return kv4_rows("k_kv4_store", false, cache, k, ldk, v, ldv, dtype, rows, bias, slots, as_stream(stream));
+}
+
+int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, void* k, int64_t ldk, void* v,
+                int64_t ldv, int dtype, float* bias, void* stream) {
+  return kv4_rows("k_kv4_load", true, cache, k, ldk, v, ldv, dtype, rows, bias, slots, as_stream(stream));
+}
+
+int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ldq, int dtype,
+                            const int32_t* tables, int32_t max_pages, const int32_t* lens, int32_t nreq, int32_t hq,
+                            const float* head_gain, const float* head_temp, const float* ratio, float sm_scale,
+                            void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes, uint32_t flags,
+                            void* stream) {
+  if (flags & ~uint32_t(TG_WS_KEPT_ZERO)) return fail(TG_ERR_INVALID_ARG, "unknown flags");
+  tg::Kv4DecodeParams p{};
+  int rc = kv4_cache(cache, &p.c);
+  if (rc) return rc;
+  const int es = dtype_size(dtype);
+  if (!es) return fail(TG_ERR_INVALID_ARG, "dtype");
+  if (nreq < 0 || max_pages < 1 || hq <= 0 || hq % cache->hkv) return fail(TG_ERR_INVALID_ARG, "bad nreq / max_pages / heads");
+  const int group = hq / cache->hkv;
+  if (group > tg::kKv4MaxGroup) return fail(TG_ERR_UNSUPPORTED, "at most %d query heads per KV head", tg::kKv4MaxGroup);
+  if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
+  if (int64_t(max_pages) * cache->page_rows >= (int64_t(1) << 31))
+    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
+  if (nreq == 0) return TG_OK;
+  const int64_t width = int64_t(hq) * cache->head_dim;
+  if ((rc = check_strided("q", q, ldq, width, es)) || (rc = check_strided("out", out, ldo, width, es))) return rc;
+  if (!tables || !lens || !head_gain || !head_temp) return fail(TG_ERR_INVALID_ARG, "null pointer");
+  const size_t need = kv4_decode_ws_bytes(group, cache->head_dim);
+  if (!ws || ws_bytes < need) return fail(TG_ERR_WORKSPACE, "4-bit decode attention needs %zu workspace bytes", need);
+  if (!aligned16(ws)) return fail(TG_ERR_ALIGN, "workspace must be 16-byte aligned");
+  p.q = q;
+  p.ldq = ldq;
+  p.tables = tables;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.nreq = nreq;
+  p.hq = hq;
+  p.group = group;
+  p.gain = head_gain;
+  p.temp = head_temp;
+  p.ratio = ratio;
+  p.scale_log2 = sm_scale * tg::kLog2e;
+  p.out = out;
+  p.ldo = ldo;
+  p.lse = lse;
+  cudaStream_t st = as_stream(stream);
+  const dim3 grid(static_cast<unsigned>(nreq) * cache->hkv);
+  auto run = [&](auto kern) { return launch_pdl("k_kv4_decode_simple", kern, grid, dim3(128), 0, st, p); };
+  const bool wide = cache->head_dim == 128;
+  if (dtype == TG_BF16)
+    return wide ? run(tg::k_kv4_decode_simple<__nv_bfloat16, 128>) : run(tg::k_kv4_decode_simple<__nv_bfloat16, 64>);
+  return wide ? run(tg::k_kv4_decode_simple<float, 128>) : run(tg::k_kv4_decode_simple<float, 64>);
+}
 
 }  // extern "C"
