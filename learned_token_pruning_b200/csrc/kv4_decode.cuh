@@ -21,8 +21,8 @@
 //   fp16 (11 bits; fp32 queries carry query and weights as two fp16 parts, 22 bits).
 //   Both factors meet a power of two that keeps them in fp16's range: the query one
 //   per head (its largest value lands at 2^8), the weights one per head and scale
-//   group (weight 1 times the largest value scale met so far lands at 2^14; the
-//   running exponent moves with the running maximum of the softmax).
+//   group (weight 1 times the largest value scale met so far lands at 2^6 .. 2^7; the
+//   running exponent moves with the softmax's reference).
 //   The 8 columns hold HP heads (2, 4 or 8) times 8 / HP scale groups: with two
 //   heads, one B operand serves all four groups of D = 128.  A lane reads the
 //   accumulator columns of its own group and leaves the others.
@@ -32,9 +32,9 @@
 // Every warp streams its own run through a ring in shared memory by bulk copies
 // (a page holds a head's rows contiguously; no barrier between warps), keeps its own
 // online softmax, and writes a result directly when a (request, head) lies
-// inside its run.  Pieces of longer ones are merged per CTA in shared memory and
-// then, where they cross CTAs, by the CTA that arrives last, always in order of
-// position: reruns are bit-identical.
+// inside its run.  Pieces of longer ones are merged per CTA in shared memory and,
+// where they cross CTAs, by a second small kernel, always in order of position:
+// reruns are bit-identical.
 #pragma once
 
 #include "common.cuh"
@@ -43,9 +43,15 @@
 namespace tg {
 
 constexpr int kKv4MaxGroup = 8;
-constexpr int kKv4Warps = 8;
-constexpr int kKv4Stages = 2;
-constexpr int kKv4Tile = 64;  // keys per unit
+constexpr int kKv4Tile = 64;  // keys per unit of work
+constexpr float kKv4Slack = 8.0f;    // a weight may exceed 1 by 2^8 before the running maximum follows
+constexpr int kKv4WeightExp = 6;     // weight 1 times the largest value scale lands at 2^6 .. 2^7: 2^15 at most in fp16
+
+// warps of one CTA
+template <typename T, int HP>
+struct Kv4Cfg {
+  static constexpr int kWarps = HP == 8 || sizeof(T) == 4 ? 8 : 12;
+};
 
 struct Kv4DecodeParams {
   Kv4Cache c;
@@ -62,27 +68,30 @@ struct Kv4DecodeParams {
   void* out;
   int64_t ldo;
   float* lse;          // [nreq][hq] or null
-  float* part;         // [CTAs][2][group * (D + 2)]
-  unsigned* counters;  // [CTAs], zero between calls
+  float* part;         // [CTAs][2] pieces
 };
+
+constexpr int kKv4MinUnits = 2;      // units a CTA takes before another one joins
 
 // one piece of a (request, head): group rows of D sums, then the maxima, then the weight sums
 __host__ __device__ constexpr int kv4_piece_floats(int group, int d) { return (group * (d + 2) + 3) / 4 * 4; }
 
+// a warp's share of shared memory: two tiles of keys (codes, scales, biases), one of values
 template <int D>
-struct Kv4Stage {
+struct Kv4Ring {
   static constexpr int kCodes = kKv4Tile * D / 2, kScales = kKv4Tile * D / 16;
-  static constexpr int kVCodes = kCodes, kKScales = 2 * kCodes, kVScales = kKScales + kScales;
-  static constexpr int kBias = kVScales + kScales, kBytes = kBias + kKv4Tile * 4;
+  static constexpr int kBias = kCodes + kScales, kKeys = kBias + kKv4Tile * 4;  // in a tile of keys
+  static constexpr int kValues = 2 * kKeys, kBytes = kValues + kCodes + kScales;
 };
 
 __host__ __device__ constexpr size_t kv4_decode_head_smem(int nreq) {  // tile prefix sums
   return static_cast<size_t>(nreq + 1 + 31) / 32 * 128;
 }
-template <int D>
+template <typename T, int D, int HP>
 constexpr size_t kv4_decode_smem(int nreq, int group) {
-  return kv4_decode_head_smem(nreq) + static_cast<size_t>(kKv4Warps) * kKv4Stages * Kv4Stage<D>::kBytes +
-         static_cast<size_t>(kKv4Warps) * kv4_piece_floats(group, D) * 4;
+  using Cfg = Kv4Cfg<T, HP>;
+  return kv4_decode_head_smem(nreq) + static_cast<size_t>(Cfg::kWarps) * Kv4Ring<D>::kBytes +
+         static_cast<size_t>(Cfg::kWarps) * kv4_piece_floats(group, D) * 4;
 }
 
 __device__ __forceinline__ float kv4_ex2(float x) {
@@ -91,6 +100,27 @@ __device__ __forceinline__ float kv4_ex2(float x) {
   return y;
 }
 __device__ __forceinline__ float exp_bits(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
+
+template <int B>
+__device__ __forceinline__ uint32_t lds(uint32_t at) {  // 2 or 4 bytes of shared memory
+  uint32_t v;
+  if constexpr (B == 2) {
+    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at));
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  }
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&v)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+}
+__device__ __forceinline__ void sts_zero(uint32_t at) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory"); }
 
 // the four bytes of w (two E2M1 codes each) as fp16 pairs
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
@@ -106,6 +136,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same from a zero accumulator
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
@@ -153,27 +191,27 @@ __device__ __forceinline__ int kv4_length(const Kv4DecodeParams& p, int r) {
 }
 
 template <typename T, int D, int HP>
-__global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4DecodeParams p) {
-  using St = Kv4Stage<D>;
+__global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(const Kv4DecodeParams p) {
+  using Ring = Kv4Ring<D>;
+  constexpr int W = Kv4Cfg<T, HP>::kWarps, TP = 32 * W, MT = kKv4Tile / 16;
   constexpr bool kSplit = sizeof(T) == 4;      // fp32: query and weights in two fp16 parts
   constexpr int NG = D / 32, SL = 8 / HP, NB = NG > SL ? NG / SL : 1;
-  constexpr int S = kKv4Stages, TP = 32 * kKv4Warps;
   constexpr int kSwap = D == 128 ? 1 : 2;      // key order inside 16 rows, see below
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_full[kKv4Warps][S];
-  __shared__ int s_warp[kKv4Warps];
-  __shared__ int s_seg[kKv4Warps][2];          // (request, head) of the warp's unfinished pieces, -1: none
-  __shared__ int s_edge[kKv4Warps][2];         // bit 0: the piece begins the (request, head), bit 1: it ends it
-  __shared__ int s_stop, s_last[2];
+  __shared__ int s_warp[W];
+  __shared__ int s_seg[W][2];          // (request, head) of the warp's unfinished pieces, -1: none
+  __shared__ int s_edge[W][2];         // bit 0: the piece begins the (request, head), bit 1: it ends it
+  __shared__ uint64_t s_full[W][3];     // keys (two tiles), values
+  __shared__ int s_stop;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3, n8 = lane >> 2;
   int* s_cum = reinterpret_cast<int*>(smem);   // [nreq + 1] tiles of the requests before
-  uint8_t* ring = smem + kv4_decode_head_smem(p.nreq) + static_cast<size_t>(warp) * S * St::kBytes;
+  uint8_t* ring = smem + kv4_decode_head_smem(p.nreq) + static_cast<size_t>(warp) * Ring::kBytes;
   float* piece0 = reinterpret_cast<float*>(smem + kv4_decode_head_smem(p.nreq) +
-                                           static_cast<size_t>(kKv4Warps) * S * St::kBytes) +
+                                           static_cast<size_t>(W) * Ring::kBytes) +
                   warp * kv4_piece_floats(p.group, D);
   const int hkv = p.c.hkv, P = p.c.page_rows, group = p.group;
 
-  if (lane < S) mbar_init(&s_full[warp][lane], 1);
+  if (lane < 3) mbar_init(&s_full[warp][lane], 1);
   if (lane < 2) s_seg[warp][lane] = -1;
   if (tid == 0) s_stop = 0;
   fence_mbar_init();
@@ -198,7 +236,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
   __syncthreads();
   int base = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kKv4Warps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) base += s_warp[w];
     total += s_warp[w];
   }
@@ -216,76 +254,106 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
     for (int i = tid; i < p.hq && p.lse; i += TP) p.lse[static_cast<int64_t>(r) * p.hq + i] = -INFINITY;
   }
 
-  // ---- this warp's run of units
-  const int64_t units = static_cast<int64_t>(total) * hkv;
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), units), cta = blockIdx.x;
+  // ---- this warp's run of units: CTA c takes `each` of them, the first `more` CTAs one extra
+  const int units = total * hkv;  // < 2^31, checked by the caller
+  const int ctas = min(static_cast<int>(gridDim.x), (units + kKv4MinUnits - 1) / kKv4MinUnits), cta = blockIdx.x;
   if (cta >= ctas) return;
-  const int64_t u0 = units * cta / ctas, u1 = units * (cta + 1) / ctas;
-  const int64_t ua = u0 + (u1 - u0) * warp / kKv4Warps, ub = u0 + (u1 - u0) * (warp + 1) / kKv4Warps;
-  const int left = static_cast<int>(ub - ua);  // units to compute
+  const int each = units / ctas, more = units - each * ctas;
+  const int mine_n = each + (cta < more ? 1 : 0), u0 = each * cta + min(cta, more);
+  const int ua = u0 + mine_n * warp / W, left = u0 + mine_n * (warp + 1) / W - ua;
 
-  // position of the next unit to load: request, head, tile, the request's rows
-  const int prow = min(P, kKv4Tile), np = kKv4Tile / prow;  // rows of a page in a tile, pages in a tile
-  int lr = 0, lg = 0, lt = 0, llen = 0;
+  // position of the next unit to load: request, head, tile of the request's lnt, its rows
+  int lr = 0, lg = 0, lt = 0, lnt = 1, llen = 0;
   if (left > 0) {
     int lo = 0, hi = p.nreq - 1;  // largest request that starts at or before ua
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(s_cum[mid]) * hkv <= ua) lo = mid;
+      if (s_cum[mid] * hkv <= ua) lo = mid;
       else hi = mid - 1;
     }
     lr = lo;
-    const int nt = s_cum[lr + 1] - s_cum[lr];
-    const int x = static_cast<int>(ua - static_cast<int64_t>(s_cum[lr]) * hkv);
-    lg = x / nt;
-    lt = x - lg * nt;
+    lnt = s_cum[lr + 1] - s_cum[lr];
+    const int x = ua - s_cum[lr] * hkv;
+    lg = x / lnt;
+    lt = x - lg * lnt;
     llen = kv4_length(p, lr);
   }
-  int cr = lr, cg = lg, ct = lt, clen = llen;  // position of the unit being computed
-  auto advance = [&](int& r, int& g, int& tt, int& len) {
-    if (++tt < (len + kKv4Tile - 1) / kKv4Tile) return;
+  int cr = lr, cg = lg, ct = lt, cnt = lnt, clen = llen;  // position of the unit being computed
+  auto next_head = [&](int& r, int& g, int& tt, int& nt, int& len) {
     tt = 0;
     if (++g < hkv) return;
     g = 0;
     do ++r; while (r < p.nreq && s_cum[r + 1] == s_cum[r]);
-    len = r < p.nreq ? kv4_length(p, r) : 0;
+    if (r < p.nreq) {
+      nt = s_cum[r + 1] - s_cum[r];
+      len = kv4_length(p, r);
+    }
   };
-  // lane i moves array i / np of page i % np: K codes, V codes, K scales, V scales, biases
-  const int what = lane / np, piece = lane % np;
-  auto page_id = [&](int r, int tt, int len) -> int32_t {
-    const int row = tt * kKv4Tile + piece * prow;
-    if (what > 4 || row >= len) return 0;
-    return p.tables[static_cast<int64_t>(r) * p.max_pages + (row >> p.c.page_shift)];
+  // Lane i moves array i / MT, from 16-row block i % MT on, up to the end of the page or of
+  // the tile: K codes, K scales, biases, V codes, V scales
+  const int what = lane / MT, blk = lane % MT;
+  const bool keys = what < (p.c.bias ? 3 : 2), values = what == 3 || what == 4;
+  const uint32_t row_bytes = what == 0 || what == 3 ? D / 2 : what == 2 ? 4 : D / 16;
+  const uint8_t* src0 = what == 0   ? p.c.k_codes
+                        : what == 1 ? reinterpret_cast<const uint8_t*>(p.c.k_scales)
+                        : what == 2 ? reinterpret_cast<const uint8_t*>(p.c.bias)
+                        : what == 3 ? p.c.v_codes
+                                    : reinterpret_cast<const uint8_t*>(p.c.v_scales);
+  uint8_t* dst0 = ring + blk * 16 * row_bytes +
+                  (what == 0 ? 0 : what == 1 ? Ring::kCodes : what == 2 ? Ring::kBias : what == 3 ? Ring::kValues : Ring::kValues + Ring::kCodes);
+  const int64_t page_bytes = static_cast<int64_t>(what == 2 ? 1 : hkv) * P * row_bytes;
+  const uint32_t head_bytes = what == 2 ? 0 : P * row_bytes;  // biases are shared by the heads
+  const uint32_t key_tx = 16 * (D / 2 + D / 16 + (p.c.bias ? 4 : 0)), value_tx = 16 * (D / 2 + D / 16);
+  const uint32_t full0 = smem_u32(&s_full[warp][0]);
+  // The request's next 32 page ids, one per lane: fetched when the position moves past
+  // them or to another request, used by a later load.
+  int32_t pages = 0;
+  int page0 = 0;
+  auto fetch_pages = [&]() {
+    page0 = (lt * kKv4Tile) >> p.c.page_shift;
+    pages = 0;
+    if (lr < p.nreq && (page0 + lane) << p.c.page_shift < llen)
+      pages = p.tables[static_cast<int64_t>(lr) * p.max_pages + page0 + lane];
   };
-  auto load = [&](int st, int r, int g, int tt, int len, int32_t page) {
-    const int rows = min(kKv4Tile, len - tt * kKv4Tile), pieces = (rows + prow - 1) / prow;
-    if (lane == 0)
-      mbar_arrive_expect_tx(&s_full[warp][st], pieces * prow * (D + D / 8 + (p.c.bias ? 4 : 0)));
+  // The keys of the next tile into key tile `st`; where its values are is kept for load_values,
+  // one tile behind (blocks of both, this lane's source and size)
+  const uint8_t* vsrc0 = nullptr;
+  const uint8_t* vsrc1 = nullptr;
+  uint32_t vbytes0 = 0, vbytes1 = 0;
+  int vblocks0 = 0, vblocks1 = 0;
+  auto load_values = [&]() {
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][2], vblocks0 * value_tx);
     __syncwarp();
-    if (what <= (p.c.bias ? 4 : 3) && piece < pieces) {
+    if (values && vbytes0) bulk_load(dst0, vsrc0, vbytes0, &s_full[warp][2]);
+    vsrc0 = vsrc1;
+    vbytes0 = vbytes1;
+    vblocks0 = vblocks1;
+  };
+  auto load_keys = [&](int st) {
+    const int row0 = lt * kKv4Tile, blocks = min(MT, (llen - row0 + 15) >> 4);
+    const int row = row0 + 16 * blk, in_page = row & (P - 1);
+    int32_t page = __shfl_sync(0xffffffffu, pages, (row >> p.c.page_shift) - page0);
+    if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][st], blocks * key_tx);
+    __syncwarp();
+    uint32_t bytes = 0;
+    if (blk < blocks && (blk == 0 || in_page == 0)) {
       if (page < 0 || page >= p.c.num_pages) {
         raise_error(kErrKvPage, 2);
         page = 0;
       }
-      const int off = (tt * kKv4Tile) & (P - 1);  // 0 unless a page holds several tiles
-      const int64_t row = ((static_cast<int64_t>(page) * hkv + g) << p.c.page_shift) + off;
-      uint8_t* dst = ring + st * St::kBytes;
-      const void* src;
-      uint32_t bytes;
-      if (what < 2) {
-        src = (what ? p.c.v_codes : p.c.k_codes) + row * (D / 2);
-        bytes = prow * (D / 2);
-        dst += what * St::kVCodes + piece * bytes;
-      } else if (what < 4) {
-        src = (what == 3 ? p.c.v_scales : p.c.k_scales) + row * (D / 32);
-        bytes = prow * (D / 16);
-        dst += (what == 3 ? St::kVScales : St::kKScales) + piece * bytes;
-      } else {
-        src = p.c.bias + ((static_cast<int64_t>(page) << p.c.page_shift) + off);
-        bytes = prow * 4;
-        dst += St::kBias + piece * bytes;
-      }
-      bulk_load(dst, src, bytes, &s_full[warp][st]);
+      bytes = min(blocks - blk, (P - in_page) >> 4) * 16 * row_bytes;
+    }
+    const uint8_t* src = src0 + page * page_bytes + lg * static_cast<uint64_t>(head_bytes) + in_page * row_bytes;
+    if (keys && bytes) bulk_load(dst0 + st * Ring::kKeys, src, bytes, &s_full[warp][st]);
+    vsrc1 = src;
+    vbytes1 = bytes;
+    vblocks1 = blocks;
+    if (++lt == lnt) {
+      const int r = lr;
+      next_head(lr, lg, lt, lnt, llen);
+      if (lr != r || page0 != 0) fetch_pages();
+    } else if (((lt * kKv4Tile + kKv4Tile - 1) >> p.c.page_shift) - page0 >= 32) {
+      fetch_pages();
     }
   };
 
@@ -298,9 +366,15 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
   // rows 2t, 2t + 1, 2t + 8, 2t + 9).
   const int key0 = n8 & 1 ? 4 + ((n8 >> 1) ^ kSwap) : n8 >> 1;
   const int kswz = D == 128 ? (key0 & 2) << 4 : 0, vswz = D == 128 ? (t & 2) << 4 : 0;
-  const uint32_t kbase = smem_u32(ring) + key0 * (D / 2) + ((t * (D / 8)) ^ kswz);
-  const uint32_t vbase = smem_u32(ring) + St::kVCodes + ((n8 * (D / 16)) ^ vswz);
-  const int va = t, vb = 4 + (t ^ kSwap);
+  const uint32_t ring_at = smem_u32(ring);
+  const uint32_t kbase = ring_at + key0 * (D / 2) + ((t * (D / 8)) ^ kswz);
+  const uint32_t vbase = ring_at + Ring::kValues + ((n8 * (D / 16)) ^ vswz) + t * (D / 2);  // key t of 16
+  const uint32_t vother = (4 + (t ^ kSwap) - t) * (D / 2);                                // to its odd row's key
+  const uint32_t sbase = ring_at + Ring::kCodes + key0 * (D / 16);
+  const uint32_t wbase = ring_at + Ring::kValues + Ring::kCodes + key0 * (D / 16) + 2 * slot;
+  const uint32_t bbase = ring_at + Ring::kBias + 4 * key0;
+  if (!p.c.bias)  // no copy writes the biases then
+    for (int i = lane; i < 2 * kKv4Tile; i += 32) sts_zero(ring_at + i / kKv4Tile * Ring::kKeys + Ring::kBias + i % kKv4Tile * 4);
 
   uint32_t qf[kSplit ? 2 : 1][NG][2][2];
   float o[NG][2][4];
@@ -346,7 +420,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.0f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) ex[b] = 15;  // 2^(141 - ex) and its inverse are both normal floats from here on
+    for (int b = 0; b < NB; ++b) ex[b] = kKv4WeightExp + 1;  // from here on the weights' factor and its inverse are normal floats
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -367,7 +441,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (g % SL != slot) continue;
-      const float unit = exp_bits(ex[g / SL] - 14);  // 2^(ex - 141)
+      const float unit = exp_bits(ex[g / SL] - kKv4WeightExp);  // the inverse of the weights' factor
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (hd + c >= group) continue;
@@ -396,71 +470,76 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
 
   bool ok = true;
   if (left > 0) {
-    // fill the ring: the page ids first, so that their loads overlap
-    int32_t first_page[S], next_page = 0;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      first_page[i] = i < left ? page_id(lr, lt, llen) : 0;
-      if (i < left) advance(lr, lg, lt, llen);
-    }
-    if (S < left) next_page = page_id(lr, lt, llen);
-    int fr = cr, fg = cg, ft = ct, flen = clen;
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      if (i < left) {
-        load(i, fr, fg, ft, flen, first_page[i]);
-        advance(fr, fg, ft, flen);
-      }
-    }
-    bool first_unit = true;
-    int begun = ct == 0;  // the current (request, head) begins in this run
+    fetch_pages();
+    load_keys(0);
+    vsrc0 = vsrc1, vbytes0 = vbytes1, vblocks0 = vblocks1;
+    if (left > 1) load_keys(1);
+    load_values();
+    bool begun = ct == 0;  // the current (request, head) begins in this run
+    bool fresh = true;     // its state is not set up yet
+#pragma unroll 1
     for (int i = 0; i < left; ++i) {
-      if (first_unit || ct == 0) begin();
-      first_unit = false;
-      const int st = i % S;
-      ok = warp_wait(&s_full[warp][st], (i / S) & 1, kErrWaitAttention);
-      if (!ok) break;
-      const uint32_t stage = st * St::kBytes;
-      const uint8_t* sp = ring + stage;
+      if (fresh) begin();
+      fresh = false;
+      const uint32_t st = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(full0 + 8 * st, i >> 1 & 1))) {
+        ok = warp_wait(&s_full[warp][st], i >> 1 & 1, kErrWaitAttention);
+        if (!ok) break;
+      }
+      const uint32_t stage = st * Ring::kKeys;
       const int rows = min(kKv4Tile, clen - ct * kKv4Tile);
+      // Keys past the request's rows and keys with bias -infinity: their scales and biases
+      // are zeroed (whatever they hold must not meet the sums) and their logits set to -infinity.
+      uint32_t dead[(MT + 1) / 2];
+      bool any_dead = false;
+#pragma unroll
+      for (int h = 0; h < (MT + 1) / 2; ++h) {
+        const int key = 32 * h + lane;
+        bool d = false;
+        if (key < kKv4Tile) d = key >= rows || __uint_as_float(lds<4>(ring_at + stage + Ring::kBias + 4 * key)) == -INFINITY;
+        dead[h] = __ballot_sync(0xffffffffu, d);
+        any_dead |= dead[h] != 0;
+      }
+      if (any_dead) {
+#pragma unroll
+        for (int h = 0; h < (MT + 1) / 2; ++h)
+          if (dead[h] >> lane & 1u) {
+            const uint32_t key = 32 * h + lane;
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g) sts_zero(ring_at + stage + Ring::kCodes + key * (D / 16) + 4 * g);
+            sts_zero(ring_at + stage + Ring::kBias + 4 * key);
+          }
+        fence_proxy_async_smem();  // before the next copy into this tile
+        __syncwarp();
+      }
 
-      // ---- scores of 64 keys
-      float x[4][4];
-      bool live0[4], live1[4];
+      // ---- scores of the tile's keys
+      float x[MT][4];
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
         uint32_t w0[NG], w1[NG];  // halves (unit 2t: groups 0..), (unit 2t + 1: groups 0..)
-        const uint32_t ka = kbase + stage + mt * 16 * (D / 2);
-        if constexpr (D == 128) {
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(ka));
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(ka + 8 * (D / 2)));
-        } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(ka));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(ka + 8 * (D / 2)));
-        }
+        const uint32_t ka = kbase + stage + mt * 8 * D;
+        lds_words(ka, w0);
+        lds_words(ka + 4 * D, w1);
         uint32_t h0[NG][4], h1[NG][4];  // [word][byte]: word s * NG / 2 + g / 2, bytes 2 (g & 1), + 1
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
           e2m1x8(w0[w], h0[w]);
           e2m1x8(w1[w], h1[w]);
         }
-        const int key = mt * 16 + key0;
         uint32_t sc0[NG / 2], sc1[NG / 2];  // bf16 scale pairs of both keys
-#pragma unroll
-        for (int g = 0; g < NG / 2; ++g) {
-          sc0[g] = *reinterpret_cast<const uint32_t*>(sp + St::kKScales + key * (D / 16) + 4 * g);
-          sc1[g] = *reinterpret_cast<const uint32_t*>(sp + St::kKScales + (key + 8) * (D / 16) + 4 * g);
-        }
+        lds_words(sbase + stage + mt * D, sc0);
+        lds_words(sbase + stage + mt * D + D / 2, sc1);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float acc[4];
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const int w = s * (NG / 2) + g / 2, b = 2 * (g & 1);
-#pragma unroll
-            for (int v = 0; v < (kSplit ? 2 : 1); ++v)
-              mma_f16(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[v][g][s][0], qf[v][g][s][1]);
+            if (s == 0) mma_f16_zero(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[0][g][0][0], qf[0][g][0][1]);
+            else mma_f16(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[0][g][1][0], qf[0][g][1][1]);
+            if constexpr (kSplit) mma_f16(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[1][g][s][0], qf[1][g][s][1]);
           }
           const float k0 = g & 1 ? bf16_hi(sc0[g / 2]) : bf16_lo(sc0[g / 2]);
           const float k1 = g & 1 ? bf16_hi(sc1[g / 2]) : bf16_lo(sc1[g / 2]);
@@ -469,80 +548,97 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
           x[mt][2] = g ? fmaf(k1, acc[2], x[mt][2]) : k1 * acc[2];
           x[mt][3] = g ? fmaf(k1, acc[3], x[mt][3]) : k1 * acc[3];
         }
-        float bias0 = 0.0f, bias1 = 0.0f;
-        if (p.c.bias) {
-          bias0 = *reinterpret_cast<const float*>(sp + St::kBias + 4 * key);
-          bias1 = *reinterpret_cast<const float*>(sp + St::kBias + 4 * key + 32);
+        const float bias0 = __uint_as_float(lds<4>(bbase + stage + 64 * mt));
+        const float bias1 = __uint_as_float(lds<4>(bbase + stage + 64 * mt + 32));
+        x[mt][0] = fmaf(a0, x[mt][0], g0 * bias0);
+        x[mt][1] = fmaf(a1, x[mt][1], g1 * bias0);
+        x[mt][2] = fmaf(a0, x[mt][2], g0 * bias1);
+        x[mt][3] = fmaf(a1, x[mt][3], g1 * bias1);
+      }
+      if (any_dead) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t m = dead[mt / 2] >> (16 * (mt & 1) + key0);
+          if (m & 1u) x[mt][0] = x[mt][1] = -INFINITY;
+          if (m >> 8 & 1u) x[mt][2] = x[mt][3] = -INFINITY;
         }
-        live0[mt] = key < rows && bias0 != -INFINITY;
-        live1[mt] = key + 8 < rows && bias1 != -INFINITY;
-        x[mt][0] = live0[mt] ? fmaf(a0, x[mt][0], g0 * bias0) : -INFINITY;
-        x[mt][1] = live0[mt] ? fmaf(a1, x[mt][1], g1 * bias0) : -INFINITY;
-        x[mt][2] = live1[mt] ? fmaf(a0, x[mt][2], g0 * bias1) : -INFINITY;
-        x[mt][3] = live1[mt] ? fmaf(a1, x[mt][3], g1 * bias1) : -INFINITY;
+      }
+      __syncwarp();  // every lane has read the keys
+      if (i + 2 < left) load_keys(st);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
         t0 = fmaxf(t0, fmaxf(x[mt][0], x[mt][2]));
         t1 = fmaxf(t1, fmaxf(x[mt][1], x[mt][3]));
       }
 
       // ---- running maxima of the logits and of the value scales' exponents
-      uint32_t vs0[4][NB], vs1[4][NB];  // bf16 value scales of this lane's groups, as fp32 bits
+      if (!__all_sync(0xffffffffu, mbar_try_wait(full0 + 16, i & 1))) {
+        ok = warp_wait(&s_full[warp][2], i & 1, kErrWaitAttention);
+        if (!ok) break;
+      }
+      if (any_dead) {
+#pragma unroll
+        for (int h = 0; h < (MT + 1) / 2; ++h)
+          if (dead[h] >> lane & 1u)
+#pragma unroll
+            for (int g = 0; g < NG / 2; ++g)
+              sts_zero(ring_at + Ring::kValues + Ring::kCodes + (32 * h + lane) * (D / 16) + 4 * g);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      uint32_t vs0[MT][NB], vs1[MT][NB];  // bf16 value scales of this lane's groups, as fp32 bits
       uint32_t vtop[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) vtop[b] = 0;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const int key = mt * 16 + key0, g = b * SL + slot;
-          const uint32_t s0 = *reinterpret_cast<const uint16_t*>(sp + St::kVScales + key * (D / 16) + 2 * g);
-          const uint32_t s1 = *reinterpret_cast<const uint16_t*>(sp + St::kVScales + (key + 8) * (D / 16) + 2 * g);
-          vs0[mt][b] = live0[mt] ? s0 << 16 : 0u;
-          vs1[mt][b] = live1[mt] ? s1 << 16 : 0u;
+          vs0[mt][b] = lds<2>(wbase + mt * D + 2 * SL * b) << 16;
+          vs1[mt][b] = lds<2>(wbase + mt * D + D / 2 + 2 * SL * b) << 16;
           vtop[b] = max(vtop[b], max(vs0[mt][b], vs1[mt][b]));
         }
-      t0 = rows_max(t0);
-      t1 = rows_max(t1);
-      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-      bool moved = n0 != m0 || n1 != m1;
-      int nex[NB];
+      // The reference m and the unit of the weights move only when a logit passes m by
+      // 2^8 or a value scale has a larger exponent (a warp vote; the first tile always does).
+      bool moved = t0 > m0 + kKv4Slack || t1 > m1 + kKv4Slack;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t v = vtop[b];
-        v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = max(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        nex[b] = max(ex[b], min(static_cast<int>(v >> 23), 254));  // NaN scales (255) set no unit
-        moved |= nex[b] != ex[b];
-      }
-      const float use0 = n0 == -INFINITY ? 0.0f : n0, use1 = n1 == -INFINITY ? 0.0f : n1;
+      for (int b = 0; b < NB; ++b) moved |= static_cast<int>(vtop[b] >> 23) > ex[b];
       if (__any_sync(0xffffffffu, moved)) {
-        const float d0 = m0 - use0, d1 = m1 - use1;
+        const float n0 = fmaxf(m0, rows_max(t0)), n1 = fmaxf(m1, rows_max(t1));
+        const float d0 = n0 == m0 ? 0.0f : m0 - n0, d1 = n1 == m1 ? 0.0f : m1 - n1;
         l0 *= kv4_ex2(d0);
         l1 *= kv4_ex2(d1);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const float de = static_cast<float>(ex[g / SL] - nex[g / SL]);
+        for (int b = 0; b < NB; ++b) {
+          uint32_t v = vtop[b];
+          v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = max(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          const int nex = max(ex[b], min(static_cast<int>(v >> 23), 254));  // NaN scales (255) set no unit
+          const float de = static_cast<float>(ex[b] - nex);
           const float c0 = kv4_ex2(d0 + de), c1 = kv4_ex2(d1 + de);
+          ex[b] = nex;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            o[g][j][0] *= c0;
-            o[g][j][1] *= c1;
-            o[g][j][2] *= c0;
-            o[g][j][3] *= c1;
-          }
+          for (int g = b * SL; g < (b + 1) * SL && g < NG; ++g)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              o[g][j][0] *= c0;
+              o[g][j][1] *= c1;
+              o[g][j][2] *= c0;
+              o[g][j][3] *= c1;
+            }
         }
         m0 = n0;
         m1 = n1;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) ex[b] = nex[b];
       }
+      const float use0 = m0 == -INFINITY ? 0.0f : m0, use1 = m1 == -INFINITY ? 0.0f : m1;
       float fac[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) fac[b] = exp_bits(268 - ex[b]);  // 2^(141 - ex)
+      for (int b = 0; b < NB; ++b) fac[b] = exp_bits(254 + kKv4WeightExp - ex[b]);  // 2^(127 + kKv4WeightExp - ex)
 
       // ---- weights, and their products with the values
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
         const float p00 = kv4_ex2(x[mt][0] - use0), p01 = kv4_ex2(x[mt][1] - use1);
         const float p10 = kv4_ex2(x[mt][2] - use0), p11 = kv4_ex2(x[mt][3] - use1);
         l0 += p00 + p10;
@@ -560,19 +656,12 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
             pf[1][b][1] = transpose8x8(f16x2(w10 - f16_lo(r1), w11 - f16_hi(r1)));
           }
         }
-        const uint32_t va0 = vbase + stage + (mt * 16 + va) * (D / 2), vb0 = vbase + stage + (mt * 16 + vb) * (D / 2);
+        const uint32_t va = vbase + mt * 8 * D;
         uint32_t wa[NG / 2], wb[NG / 2], wc[NG / 2], wd[NG / 2];
-        if constexpr (D == 128) {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wa[0]), "=r"(wa[1]) : "r"(va0));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wb[0]), "=r"(wb[1]) : "r"(vb0));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wc[0]), "=r"(wc[1]) : "r"(va0 + 8 * (D / 2)));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(wd[0]), "=r"(wd[1]) : "r"(vb0 + 8 * (D / 2)));
-        } else {
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wa[0]) : "r"(va0));
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wb[0]) : "r"(vb0));
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wc[0]) : "r"(va0 + 8 * (D / 2)));
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(wd[0]) : "r"(vb0 + 8 * (D / 2)));
-        }
+        lds_words(va, wa);
+        lds_words(va + vother, wb);
+        lds_words(va + 4 * D, wc);
+        lds_words(va + vother + 4 * D, wd);
 #pragma unroll
         for (int w = 0; w < NG / 2; ++w) {
           // low nibbles of two keys side by side, then the high ones: byte 2i + j holds
@@ -593,130 +682,211 @@ __global__ void __launch_bounds__(32 * kKv4Warps, 1) k_kv4_decode(const Kv4Decod
                         pf[v][(2 * w + i) / SL][0], pf[v][(2 * w + i) / SL][1]);
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (i + S < left) {
-        load(st, lr, lg, lt, llen, next_page);
-        advance(lr, lg, lt, llen);
-        if (i + S + 1 < left) next_page = page_id(lr, lt, llen);
-      }
-      const bool ends = (ct + 1) * kKv4Tile >= clen;
+      __syncwarp();  // every lane has read the values
+      if (i + 1 < left) load_values();
+      const bool ends = ct + 1 == cnt;
       if (ends || i + 1 == left) {
         if (begun && ends) {
           finish(true, nullptr);
         } else {
           // a piece: one that begins here ends the run, so the ring is free for it
-          float* dst = begun ? reinterpret_cast<float*>(ring) : piece0;
-          finish(false, dst);
+          finish(false, begun ? reinterpret_cast<float*>(ring) : piece0);
           if (lane == 0) {
             s_seg[warp][begun] = cr * hkv + cg;
             s_edge[warp][begun] = begun | (ends ? 2 : 0);
           }
         }
-        begun = 1;
+        begun = fresh = true;
       }
-      advance(cr, cg, ct, clen);
+      if (ends) next_head(cr, cg, ct, cnt, clen);
+      else ++ct;
     }
   }
   if (!ok && lane == 0) s_stop = 1;
   __syncthreads();
   if (s_stop) return;  // a wait ran out (recorded in the error word)
 
-  // ---- pieces of this CTA, in order of position, to the output or to the workspace
-  const int pf4 = kv4_piece_floats(group, D);
-  float* pieces = reinterpret_cast<float*>(smem + kv4_decode_head_smem(p.nreq) +
-                                           static_cast<size_t>(kKv4Warps) * S * St::kBytes);
-  auto piece_at = [&](int i) -> const float* {  // piece i: warp i / 2, slot i % 2
-    return i & 1 ? reinterpret_cast<const float*>(smem + kv4_decode_head_smem(p.nreq) +
-                                                  static_cast<size_t>(i >> 1) * S * St::kBytes)
-                 : pieces + (i >> 1) * pf4;
+  // ---- pieces of this CTA, in order of position, to the output or to the workspace.
+  // Every warp walks the list (piece 2w is what warp w continued, 2w + 1 what it began);
+  // a thread takes four neighbouring values.
+  const int pf = kv4_piece_floats(group, D), vals = group * D;
+  const int my_seg = lane < 2 * W ? s_seg[lane >> 1][lane & 1] : -1;
+  const int my_edge = lane < 2 * W ? s_edge[lane >> 1][lane & 1] : 0;
+  const uint8_t* rings = smem + kv4_decode_head_smem(p.nreq);
+  const float* kept = reinterpret_cast<const float*>(rings + static_cast<size_t>(W) * Ring::kBytes);
+  auto piece_at = [&](int i) -> const float* {
+    return i & 1 ? reinterpret_cast<const float*>(rings + static_cast<size_t>(i >> 1) * Ring::kBytes) : kept + (i >> 1) * pf;
   };
-  int open[2] = {-1, -1};  // (request, head) continued from an earlier CTA, and into a later one
-  for (int i = 0; i < 2 * kKv4Warps;) {
-    const int seg = s_seg[i >> 1][i & 1];
-    if (seg < 0) {
-      ++i;
-      continue;
+  // four values, the reference and the weight sum of head u: to the output, or kept as a piece
+  auto emit = [&](int seg, bool whole, float* dst, int e, int u, float4 y, float top, float sum) {
+    if (!whole) {
+      *reinterpret_cast<float4*>(dst + e) = y;
+      if (e % D == 0) {
+        dst[vals + u] = top;
+        dst[vals + group + u] = sum;
+      }
+      return;
     }
-    int end = i + 1, last = i;
-    while (end < 2 * kKv4Warps && (s_seg[end >> 1][end & 1] == seg || s_seg[end >> 1][end & 1] < 0)) {
-      if (s_seg[end >> 1][end & 1] == seg) last = end;
-      ++end;
-    }
-    const bool begins = s_edge[i >> 1][i & 1] & 1, whole = begins && (s_edge[last >> 1][last & 1] & 2);
     const int r = seg / hkv, h0 = seg % hkv * group;
-    float* part = p.part + (cta * 2 + (begins ? 1 : 0)) * pf4;
-    for (int e = tid; e < group * D; e += TP) {
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    store4(static_cast<T*>(p.out) + r * p.ldo + static_cast<int64_t>(h0) * D + e, y.x * f, y.y * f, y.z * f, y.w * f);
+    if (e % D == 0 && p.lse)
+      p.lse[static_cast<int64_t>(r) * p.hq + h0 + u] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  };
+  for (uint32_t todo = __ballot_sync(0xffffffffu, my_seg >= 0); todo;) {
+    const int i = __ffs(todo) - 1, seg = __shfl_sync(0xffffffffu, my_seg, i);
+    const uint32_t members = __ballot_sync(0xffffffffu, my_seg == seg);
+    todo &= ~members;
+    const bool begins = __shfl_sync(0xffffffffu, my_edge, i) & 1;
+    const bool whole = begins && (__shfl_sync(0xffffffffu, my_edge, 31 - __clz(members)) & 2);
+    for (int e = 4 * tid; e < vals; e += 4 * TP) {
       const int u = e / D;
       float top = -INFINITY;
-      for (int k = i; k <= last; ++k)
-        if (s_seg[k >> 1][k & 1] == seg) top = fmaxf(top, piece_at(k)[group * D + u]);
+      for (uint32_t m = members; m; m &= m - 1) top = fmaxf(top, piece_at(__ffs(m) - 1)[vals + u]);
       const float use = top == -INFINITY ? 0.0f : top;
-      float y = 0.0f, sum = 0.0f;
-      for (int k = i; k <= last; ++k)
-        if (s_seg[k >> 1][k & 1] == seg) {
-          const float* pc = piece_at(k);
-          const float f = kv4_ex2(pc[group * D + u] - use);
-          y = fmaf(f, pc[e], y);
-          sum = fmaf(f, pc[group * (D + 1) + u], sum);
-        }
-      if (whole) {
-        static_cast<T*>(p.out)[r * p.ldo + static_cast<int64_t>(h0) * D + e] = from_f32<T>(sum == 0.0f ? 0.0f : y / sum);
-        if (e % D == 0 && p.lse)
-          p.lse[static_cast<int64_t>(r) * p.hq + h0 + u] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        part[e] = y;
-        if (e % D == 0) {
-          part[group * D + u] = top;
-          part[group * (D + 1) + u] = sum;
-        }
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+      for (uint32_t m = members; m; m &= m - 1) {
+        const float* pc = piece_at(__ffs(m) - 1);
+        const float f = kv4_ex2(pc[vals + u] - use);
+        const float4 v = *reinterpret_cast<const float4*>(pc + e);
+        y.x = fmaf(f, v.x, y.x);
+        y.y = fmaf(f, v.y, y.y);
+        y.z = fmaf(f, v.z, y.z);
+        y.w = fmaf(f, v.w, y.w);
+        sum = fmaf(f, pc[vals + group + u], sum);
       }
+      emit(seg, whole, p.part + (static_cast<int64_t>(cta) * 2 + begins) * pf, e, u, y, top, sum);
     }
-    if (!whole) open[begins] = seg;
-    i = end;
   }
 
-  // ---- (request, head)s that cross CTAs: the last CTA to arrive adds the parts in CTA order
-  if (open[0] < 0 && open[1] < 0) return;
-  __threadfence();
-  __syncthreads();
-  int64_t c0[2], c1[2];
+}
+
+// The (request, head)s that cross CTAs of k_kv4_decode: block c adds the parts of the one
+// that begins in CTA c and goes on after it, in CTA order (blocks without one return).  Block
+// row y takes 256 of the group * D values: 4 slices of the parts side by side, 64 threads each.
+// Launched right behind the main kernel: the plan is formed while that one still runs.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_kv4_merge(const Kv4DecodeParams p, int ctas_max) {
+  constexpr int kVals = 256, kHeads = kVals / D, kAhead = 6;
+  extern __shared__ float s_w[];  // [CTAs][kHeads] weights
+  __shared__ int s_warp[8], s_find[3];
+  __shared__ float s_top[kHeads], s_sum[kHeads];
+  __shared__ float4 s_y[256];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hkv = p.c.hkv, vals = p.group * D;
+  // the kernels before the main one are done: it began this launch after its own wait for them
+  const int per = (p.nreq + 255) / 256, rq0 = min(tid * per, p.nreq), rq1 = min(rq0 + per, p.nreq);
+  int mine = 0;
+  for (int r = rq0; r < rq1; ++r) mine += (kv4_length(p, r) + kKv4Tile - 1) / kKv4Tile;
+  int inc = mine;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int r = max(open[k], 0) / hkv, g = max(open[k], 0) % hkv;
-    const int nt = s_cum[r + 1] - s_cum[r];
-    const int64_t first = static_cast<int64_t>(s_cum[r]) * hkv + static_cast<int64_t>(g) * nt;
-    c0[k] = ((first + 1) * ctas - 1) / units;     // CTA of a unit u: the largest c with units * c / ctas <= u
-    c1[k] = ((first + nt) * ctas - 1) / units;
-    if (tid == 0)
-      s_last[k] = open[k] >= 0 && atomicAdd(&p.counters[c0[k]], 1u) == static_cast<unsigned>(c1[k] - c0[k]);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  if (tid == 0) s_find[0] = -1;
+  __syncthreads();
+  int base = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) base += s_warp[w];
+    total += s_warp[w];
+  }
+  const int units = total * hkv, ctas = min(ctas_max, (units + kKv4MinUnits - 1) / kKv4MinUnits), cta = blockIdx.x;
+  // a block leaves only after the main kernel: the next launch waits for this one alone
+  if (cta + 1 >= ctas) {
+    pdl_wait();
+    return;
+  }
+  const int each = units / ctas, more = units - each * ctas;
+  const int u0 = each * cta + min(cta, more), end = u0 + each + (cta < more ? 1 : 0);
+  // the request of the CTA's last unit
+  for (int r = rq0; r < rq1; ++r) {
+    const int n = (kv4_length(p, r) + kKv4Tile - 1) / kKv4Tile;
+    if (n && base * hkv < end && end <= (base + n) * hkv) {
+      s_find[0] = r;
+      s_find[1] = base;
+      s_find[2] = n;
+    }
+    base += n;
   }
   __syncthreads();
+  const int r = s_find[0], nt = s_find[2];
+  const int g = (end - 1 - s_find[1] * hkv) / nt, first = s_find[1] * hkv + g * nt, stop = first + nt;
+  if (first < u0 || stop <= end) {  // begun earlier, or finished here
+    pdl_wait();
+    return;
+  }
+  const int last = stop - 1 < more * (each + 1) ? (stop - 1) / (each + 1) : more + (stop - 1 - more * (each + 1)) / each;
+  const int parts = last - cta + 1, pf = kv4_piece_floats(p.group, D);
+  const int v0 = blockIdx.y * kVals, h0 = v0 / D;  // this block's values and heads of the group
+  // part 0: slot 1 of the CTA it begins in, then slot 0 of those after it
+  auto part_at = [&](int j) { return p.part + (static_cast<int64_t>(cta + j) * 2 + (j == 0 ? 1 : 0)) * pf; };
+  pdl_wait();
+  pdl_launch_dependents();
+  const int e = v0 + 4 * (tid & 63), sl = tid >> 6;
+  const bool in = e < vals;
+  float4 ahead[kAhead];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!s_last[k]) continue;
-    __threadfence();
-    const int r = open[k] / hkv, h0 = open[k] % hkv * group, cnt = static_cast<int>(c1[k] - c0[k]) + 1;
-    const float* first = p.part + (c0[k] * 2 + 1) * pf4;          // begins in CTA c0: its slot 1
-    const float* rest = p.part + (c0[k] + 1) * 2 * pf4;           // then slot 0 of the CTAs after it
-    for (int e = tid; e < group * D; e += TP) {
-      const int u = e / D;
-      float top = __ldcg(first + group * D + u);
-      for (int j = 0; j < cnt - 1; ++j) top = fmaxf(top, __ldcg(rest + static_cast<int64_t>(j) * 2 * pf4 + group * D + u));
-      const float use = top == -INFINITY ? 0.0f : top;
-      float f = kv4_ex2(__ldcg(first + group * D + u) - use);
-      float y = f * __ldcg(first + e), sum = f * __ldcg(first + group * (D + 1) + u);
-#pragma unroll 4
-      for (int j = 0; j < cnt - 1; ++j) {
-        const float* pc = rest + static_cast<int64_t>(j) * 2 * pf4;
-        f = kv4_ex2(__ldcg(pc + group * D + u) - use);
-        y = fmaf(f, __ldcg(pc + e), y);
-        sum = fmaf(f, __ldcg(pc + group * (D + 1) + u), sum);
-      }
-      static_cast<T*>(p.out)[r * p.ldo + static_cast<int64_t>(h0) * D + e] = from_f32<T>(sum == 0.0f ? 0.0f : y / sum);
-      if (e % D == 0 && p.lse)
-        p.lse[static_cast<int64_t>(r) * p.hq + h0 + u] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  for (int i = 0; i < kAhead; ++i)
+    if (in && sl + 4 * i < parts) ahead[i] = __ldcg(reinterpret_cast<const float4*>(part_at(sl + 4 * i) + e));
+  if (warp < kHeads && h0 + warp < p.group) {
+    const int u = h0 + warp;
+    float top = -INFINITY;
+    for (int j = lane; j < parts; j += 32) {
+      const float m = __ldcg(part_at(j) + vals + u);
+      s_w[j * kHeads + warp] = m;
+      top = fmaxf(top, m);
     }
-    if (tid == 0) p.counters[c0[k]] = 0u;  // ready for the next call
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.0f;
+    for (int j = lane; j < parts; j += 32) {
+      const float w = kv4_ex2(s_w[j * kHeads + warp] - (top == -INFINITY ? 0.0f : top));
+      s_w[j * kHeads + warp] = w;
+      sum = fmaf(w, __ldcg(part_at(j) + vals + p.group + u), sum);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      s_top[warp] = top;
+      s_sum[warp] = sum;
+    }
+  }
+  __syncthreads();
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int hh = (e - v0) / D;
+  auto add = [&](int j, float4 v) {
+    const float f = s_w[j * kHeads + hh];
+    y.x = fmaf(f, v.x, y.x);
+    y.y = fmaf(f, v.y, y.y);
+    y.z = fmaf(f, v.z, y.z);
+    y.w = fmaf(f, v.w, y.w);
+  };
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (sl + 4 * i < parts) add(sl + 4 * i, ahead[i]);
+#pragma unroll 6
+    for (int j = sl + 4 * kAhead; j < parts; j += 4) add(j, __ldcg(reinterpret_cast<const float4*>(part_at(j) + e)));
+  }
+  s_y[tid] = y;
+  __syncthreads();
+  if (sl == 0 && in) {
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      const float4 v = s_y[64 * k + tid];
+      y.x += v.x;
+      y.y += v.y;
+      y.z += v.z;
+      y.w += v.w;
+    }
+    const float sum = s_sum[hh], f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    store4(static_cast<T*>(p.out) + r * p.ldo + static_cast<int64_t>(g) * vals + e, y.x * f, y.y * f, y.z * f, y.w * f);
+    if (e % D == 0 && p.lse)
+      p.lse[static_cast<int64_t>(r) * p.hq + g * p.group + h0 + hh] =
+          sum == 0.0f ? -INFINITY : (s_top[hh] + log2f(sum)) * 0.6931471805599453f;
   }
 }
 

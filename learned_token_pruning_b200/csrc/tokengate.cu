@@ -1999,27 +1999,31 @@ int kv4_rows(const char* what, bool load, const tg_kv4_cache* cache, const void*
 
 }  // namespace
 
-// partial results of the CTAs (two each), then their arrival counters
-static size_t kv4_decode_part_bytes(int group, int head_dim) {
-  return (static_cast<size_t>(sm_count()) * 2 * tg::kv4_piece_floats(group, head_dim) * sizeof(float) + 255) / 256 * 256;
-}
+// partial results of the CTAs (two each)
 static size_t kv4_decode_ws_bytes(int group, int head_dim) {
-  return kv4_decode_part_bytes(group, head_dim) + (static_cast<size_t>(sm_count()) * sizeof(unsigned) + 255) / 256 * 256;
+  return (static_cast<size_t>(sm_count()) * 2 * tg::kv4_piece_floats(group, head_dim) * sizeof(float) + 255) / 256 * 256;
 }
 
 namespace {
 
+template <typename T, int D, int HP>
+int launch_kv4_decode_hp(const tg::Kv4DecodeParams& p, cudaStream_t st) {
+  int rc = set_smem(tg::k_kv4_decode<T, D, HP>, tg::kv4_decode_smem<T, D, HP>(tg::kTabMaxReq, HP));
+  if (rc) return rc;
+  const int ctas = sm_count();
+  rc = launch_pdl("k_kv4_decode", tg::k_kv4_decode<T, D, HP>, dim3(static_cast<unsigned>(ctas)),
+                  dim3(32 * tg::Kv4Cfg<T, HP>::kWarps), tg::kv4_decode_smem<T, D, HP>(p.nreq, p.group), st, p);
+  if (rc) return rc;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((p.group * D + 255) / 256));
+  return launch_pdl("k_kv4_merge", tg::k_kv4_merge<T, D>, grid, dim3(256), size_t(ctas) * (256 / D) * sizeof(float), st, p, ctas);
+}
+
 template <typename T, int D>
 int launch_kv4_decode(const tg::Kv4DecodeParams& p, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    const int rc = set_smem(kern, tg::kv4_decode_smem<D>(tg::kTabMaxReq, p.group));
-    return rc ? rc : launch_pdl("k_kv4_decode", kern, dim3(static_cast<unsigned>(sm_count())), dim3(32 * tg::kKv4Warps),
-                                tg::kv4_decode_smem<D>(p.nreq, p.group), st, p);
-  };
-  if (p.group > 4) return run(tg::k_kv4_decode<T, D, 8>);
+  if (p.group > 4) return launch_kv4_decode_hp<T, D, 8>(p, st);
   if constexpr (D == 128)
-    if (p.group <= 2) return run(tg::k_kv4_decode<T, D, 2>);
-  return run(tg::k_kv4_decode<T, D, 4>);
+    if (p.group <= 2) return launch_kv4_decode_hp<T, D, 2>(p, st);
+  return launch_kv4_decode_hp<T, D, 4>(p, st);
 }
 
 }  // namespace
@@ -2053,10 +2057,9 @@ int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ld
   if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
   if (int64_t(max_pages) * cache->page_rows >= (int64_t(1) << 31))
     return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
-  // tiles and (request, head) pairs are counted in 32 bits
-  if ((int64_t(max_pages) * cache->page_rows / tg::kKv4Tile + 1) * nreq >= (int64_t(1) << 31) ||
-      int64_t(nreq) * cache->hkv >= (int64_t(1) << 31))
-    return fail(TG_ERR_UNSUPPORTED, "nreq * max_pages or nreq * hkv is too large");
+  // units of work are counted in 32 bits
+  if ((int64_t(max_pages) * cache->page_rows / tg::kKv4Tile + 1) * nreq >= (int64_t(1) << 31) / cache->hkv)
+    return fail(TG_ERR_UNSUPPORTED, "nreq * max_pages * page_rows * hkv is too large");
   if (nreq == 0) return TG_OK;
   const int64_t width = int64_t(hq) * cache->head_dim;
   if ((rc = check_strided("q", q, ldq, width, es)) || (rc = check_strided("out", out, ldo, width, es))) return rc;
@@ -2081,9 +2084,6 @@ int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ld
   p.lse = lse;
   cudaStream_t st = as_stream(stream);
   p.part = static_cast<float*>(ws);
-  p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + kv4_decode_part_bytes(group, cache->head_dim));
-  if (!(flags & TG_WS_KEPT_ZERO) && cudaMemsetAsync(p.counters, 0, sm_count() * sizeof(unsigned), st) != cudaSuccess)
-    return fail(TG_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(cudaGetLastError()));
   const bool wide = cache->head_dim == 128;
   if (dtype == TG_BF16) return wide ? launch_kv4_decode<__nv_bfloat16, 128>(p, st) : launch_kv4_decode<__nv_bfloat16, 64>(p, st);
   return wide ? launch_kv4_decode<float, 128>(p, st) : launch_kv4_decode<float, 64>(p, st);
