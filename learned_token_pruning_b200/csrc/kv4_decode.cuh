@@ -28,7 +28,7 @@
 //   accumulator columns of its own group and leaves the others.
 //
 // Work split: the (request, KV head, 64-key tile) units are laid out in that
-// order and cut into equal runs, one per warp, so ragged batches are balanced to a tile.
+// order and cut into runs of equal cost, one per warp, so ragged batches are balanced to a tile.
 // Every warp streams its own run through a ring in shared memory by bulk copies
 // (a page holds a head's rows contiguously; no barrier between warps), keeps its own
 // online softmax, and writes a result directly when a (request, head) lies
@@ -37,6 +37,7 @@
 // reruns are bit-identical.
 #pragma once
 
+#include "attn_tc.cuh"
 #include "common.cuh"
 #include "kv4.cuh"
 
@@ -71,7 +72,7 @@ struct Kv4DecodeParams {
   float* part;         // [CTAs][2] pieces
 };
 
-constexpr int kKv4MinUnits = 2;      // units a CTA takes before another one joins
+constexpr int kKv4MinCost = 4;       // cost a CTA takes before another one joins (3 at least: see kv4_tiles_before)
 
 // one piece of a (request, head): group rows of D sums, then the maxima, then the weight sums
 __host__ __device__ constexpr int kv4_piece_floats(int group, int d) { return (group * (d + 2) + 3) / 4 * 4; }
@@ -101,26 +102,21 @@ __device__ __forceinline__ float kv4_ex2(float x) {
 }
 __device__ __forceinline__ float exp_bits(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
 
-template <int B>
-__device__ __forceinline__ uint32_t lds(uint32_t at) {  // 2 or 4 bytes of shared memory
-  uint32_t v;
-  if constexpr (B == 2) {
-    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at));
-  } else {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-  }
-  return v;
-}
+// N neighbouring words of shared memory.  Plain loads, like the matrix instructions below
+// without `volatile`: the compiler may move them past one another, which is what
+// hides their latencies.
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&v)[N]) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
-  else
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+__device__ __forceinline__ void words(const uint8_t* at, uint32_t (&v)[N]) {
+  if constexpr (N == 4) {
+    const uint4 w = *reinterpret_cast<const uint4*>(at);
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+  } else if constexpr (N == 2) {
+    const uint2 w = *reinterpret_cast<const uint2*>(at);
+    v[0] = w.x, v[1] = w.y;
+  } else {
+    v[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
 }
-__device__ __forceinline__ void sts_zero(uint32_t at) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory"); }
 
 // the four bytes of w (two E2M1 codes each) as fp16 pairs
 __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
@@ -132,7 +128,7 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -140,7 +136,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 // the same from a zero accumulator
 __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
@@ -162,7 +158,7 @@ __device__ __forceinline__ float f16_hi(uint32_t h) {
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ float rows_max(float v) {  // over the 8 lanes of a column pair
@@ -189,6 +185,12 @@ __device__ __forceinline__ int kv4_length(const Kv4DecodeParams& p, int r) {
   const int n = p.lens[r];
   return n < 0 || n > static_cast<int64_t>(p.max_pages) * p.c.page_rows ? 0 : n;
 }
+
+// The work is cut by cost: 2 for a tile and 1 more for starting on a (request, head) (its
+// query, an empty state, a result to hand over: about half a tile's time).  A run has
+// the tiles whose cost begins in it; a run of 3 inside a (request, head) has at least
+// one.  Tiles of one (request, head) of nt tiles before position z of its 2 nt + 1:
+__device__ __forceinline__ int kv4_tiles_before(int z, int nt) { return min(z == 0 ? 0 : max(1, z >> 1), nt); }
 
 template <typename T, int D, int HP>
 __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(const Kv4DecodeParams p) {
@@ -254,18 +256,30 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
     for (int i = tid; i < p.hq && p.lse; i += TP) p.lse[static_cast<int64_t>(r) * p.hq + i] = -INFINITY;
   }
 
-  // ---- this warp's run of units: CTA c takes `each` of them, the first `more` CTAs one extra
-  const int units = total * hkv;  // < 2^31, checked by the caller
-  const int ctas = min(static_cast<int>(gridDim.x), (units + kKv4MinUnits - 1) / kKv4MinUnits), cta = blockIdx.x;
-  if (cta >= ctas) return;
-  const int each = units / ctas, more = units - each * ctas;
-  const int mine_n = each + (cta < more ? 1 : 0), u0 = each * cta + min(cta, more);
-  const int ua = u0 + mine_n * warp / W, left = u0 + mine_n * (warp + 1) / W - ua;
+  // ---- this warp's run: CTA c takes `each` of the cost, the first `more` CTAs one extra
+  const int cost = (2 * total + p.nreq) * hkv;  // < 2^31, checked by the caller
+  const int ctas = min(static_cast<int>(gridDim.x), max(1, cost / kKv4MinCost)), cta = blockIdx.x;
+  if (cta >= ctas || total == 0) return;
+  const int each = cost / ctas, more = cost - each * ctas;
+  const int mine_n = each + (cta < more ? 1 : 0), x0 = each * cta + min(cta, more);
+  int tiles = 0;  // even lanes: tiles before this warp's run, odd lanes: before the next one's
+  {
+    const int x = x0 + mine_n * (warp + (lane & 1)) / W;
+    int lo = 0, hi = p.nreq - 1;  // largest request that starts at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((2 * s_cum[mid] + mid) * hkv <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    const int nt = s_cum[lo + 1] - s_cum[lo], y = x - (2 * s_cum[lo] + lo) * hkv, g = y / (2 * nt + 1);
+    tiles = s_cum[lo] * hkv + g * nt + kv4_tiles_before(y - g * (2 * nt + 1), nt);
+  }
+  const int ua = __shfl_sync(0xffffffffu, tiles, 0), left = __shfl_sync(0xffffffffu, tiles, 1) - ua;
 
   // position of the next unit to load: request, head, tile of the request's lnt, its rows
   int lr = 0, lg = 0, lt = 0, lnt = 1, llen = 0;
   if (left > 0) {
-    int lo = 0, hi = p.nreq - 1;  // largest request that starts at or before ua
+    int lo = 0, hi = p.nreq - 1;  // largest request whose tiles start at or before ua: it has some
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s_cum[mid] * hkv <= ua) lo = mid;
@@ -360,21 +374,26 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
   // ---- per-lane state.  Accumulator columns 2t, 2t + 1 are heads hd, hd + 1 of scale
   // group slot `slot`; accumulator rows n8 and n8 + 8 are keys (scores) or dimensions.
   const int hd = (2 * t) % HP, slot = 2 * t / HP;
+  // Shifts left as products with factors the compiler does not see: they go to the multiply-add
+  // pipe, and the integer pipe that the conversions share is what bounds the loop.
+  uint32_t shl4, shl16;
+  asm volatile("mov.u32 %0, 16;\n\tmov.u32 %1, 65536;" : "=r"(shl4), "=r"(shl16));
   // Row i of a score tile is key key_of(i): even rows keys i / 2, odd rows the other
   // four, ordered so that the 16-byte key loads of 8 lanes and the value loads of
   // 4 keys x 4 lanes both spread over all banks (values: lane t takes the keys of
   // rows 2t, 2t + 1, 2t + 8, 2t + 9).
   const int key0 = n8 & 1 ? 4 + ((n8 >> 1) ^ kSwap) : n8 >> 1;
   const int kswz = D == 128 ? (key0 & 2) << 4 : 0, vswz = D == 128 ? (t & 2) << 4 : 0;
-  const uint32_t ring_at = smem_u32(ring);
-  const uint32_t kbase = ring_at + key0 * (D / 2) + ((t * (D / 8)) ^ kswz);
-  const uint32_t vbase = ring_at + Ring::kValues + ((n8 * (D / 16)) ^ vswz) + t * (D / 2);  // key t of 16
-  const uint32_t vother = (4 + (t ^ kSwap) - t) * (D / 2);                                // to its odd row's key
-  const uint32_t sbase = ring_at + Ring::kCodes + key0 * (D / 16);
-  const uint32_t wbase = ring_at + Ring::kValues + Ring::kCodes + key0 * (D / 16) + 2 * slot;
-  const uint32_t bbase = ring_at + Ring::kBias + 4 * key0;
+  const uint32_t at0 = static_cast<uint32_t>(ring - smem);
+  const uint32_t kbase = at0 + key0 * (D / 2) + ((t * (D / 8)) ^ kswz);
+  const uint32_t vbase = at0 + Ring::kValues + ((n8 * (D / 16)) ^ vswz) + t * (D / 2);  // key t of 16
+  const uint32_t vother = (4 + (t ^ kSwap) - t) * (D / 2);                              // to its odd row's key
+  const uint32_t sbase = at0 + Ring::kCodes + key0 * (D / 16);
+  const uint32_t wbase = at0 + Ring::kValues + Ring::kCodes + key0 * (D / 16) + 2 * slot;
+  const uint32_t bbase = at0 + Ring::kBias + 4 * key0;
   if (!p.c.bias)  // no copy writes the biases then
-    for (int i = lane; i < 2 * kKv4Tile; i += 32) sts_zero(ring_at + i / kKv4Tile * Ring::kKeys + Ring::kBias + i % kKv4Tile * 4);
+    for (int i = lane; i < 2 * kKv4Tile; i += 32)
+      *reinterpret_cast<float*>(smem + at0 + i / kKv4Tile * Ring::kKeys + Ring::kBias + i % kKv4Tile * 4) = 0.0f;
 
   uint32_t qf[kSplit ? 2 : 1][NG][2][2];
   float o[NG][2][4];
@@ -496,7 +515,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       for (int h = 0; h < (MT + 1) / 2; ++h) {
         const int key = 32 * h + lane;
         bool d = false;
-        if (key < kKv4Tile) d = key >= rows || __uint_as_float(lds<4>(ring_at + stage + Ring::kBias + 4 * key)) == -INFINITY;
+        if (key < kKv4Tile) d = key >= rows || *reinterpret_cast<const float*>(smem + at0 + stage + Ring::kBias + 4 * key) == -INFINITY;
         dead[h] = __ballot_sync(0xffffffffu, d);
         any_dead |= dead[h] != 0;
       }
@@ -506,8 +525,9 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           if (dead[h] >> lane & 1u) {
             const uint32_t key = 32 * h + lane;
 #pragma unroll
-            for (int g = 0; g < NG / 2; ++g) sts_zero(ring_at + stage + Ring::kCodes + key * (D / 16) + 4 * g);
-            sts_zero(ring_at + stage + Ring::kBias + 4 * key);
+            for (int g = 0; g < NG / 2; ++g)
+              *reinterpret_cast<uint32_t*>(smem + at0 + stage + Ring::kCodes + key * (D / 16) + 4 * g) = 0;
+            *reinterpret_cast<float*>(smem + at0 + stage + Ring::kBias + 4 * key) = 0.0f;
           }
         fence_proxy_async_smem();  // before the next copy into this tile
         __syncwarp();
@@ -519,9 +539,9 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t w0[NG], w1[NG];  // halves (unit 2t: groups 0..), (unit 2t + 1: groups 0..)
-        const uint32_t ka = kbase + stage + mt * 8 * D;
-        lds_words(ka, w0);
-        lds_words(ka + 4 * D, w1);
+        const uint8_t* ka = smem + kbase + stage + mt * 8 * D;
+        words(ka, w0);
+        words(ka + 4 * D, w1);
         uint32_t h0[NG][4], h1[NG][4];  // [word][byte]: word s * NG / 2 + g / 2, bytes 2 (g & 1), + 1
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
@@ -529,8 +549,8 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           e2m1x8(w1[w], h1[w]);
         }
         uint32_t sc0[NG / 2], sc1[NG / 2];  // bf16 scale pairs of both keys
-        lds_words(sbase + stage + mt * D, sc0);
-        lds_words(sbase + stage + mt * D + D / 2, sc1);
+        words(smem + sbase + stage + mt * D, sc0);
+        words(smem + sbase + stage + mt * D + D / 2, sc1);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float acc[4];
@@ -541,15 +561,15 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
             else mma_f16(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[0][g][1][0], qf[0][g][1][1]);
             if constexpr (kSplit) mma_f16(acc, h0[w][b], h1[w][b], h0[w][b + 1], h1[w][b + 1], qf[1][g][s][0], qf[1][g][s][1]);
           }
-          const float k0 = g & 1 ? bf16_hi(sc0[g / 2]) : bf16_lo(sc0[g / 2]);
-          const float k1 = g & 1 ? bf16_hi(sc1[g / 2]) : bf16_lo(sc1[g / 2]);
+          const float k0 = g & 1 ? bf16_hi(sc0[g / 2]) : __uint_as_float(sc0[g / 2] * shl16);
+          const float k1 = g & 1 ? bf16_hi(sc1[g / 2]) : __uint_as_float(sc1[g / 2] * shl16);
           x[mt][0] = g ? fmaf(k0, acc[0], x[mt][0]) : k0 * acc[0];
           x[mt][1] = g ? fmaf(k0, acc[1], x[mt][1]) : k0 * acc[1];
           x[mt][2] = g ? fmaf(k1, acc[2], x[mt][2]) : k1 * acc[2];
           x[mt][3] = g ? fmaf(k1, acc[3], x[mt][3]) : k1 * acc[3];
         }
-        const float bias0 = __uint_as_float(lds<4>(bbase + stage + 64 * mt));
-        const float bias1 = __uint_as_float(lds<4>(bbase + stage + 64 * mt + 32));
+        const float bias0 = *reinterpret_cast<const float*>(smem + bbase + stage + 64 * mt);
+        const float bias1 = *reinterpret_cast<const float*>(smem + bbase + stage + 64 * mt + 32);
         x[mt][0] = fmaf(a0, x[mt][0], g0 * bias0);
         x[mt][1] = fmaf(a1, x[mt][1], g1 * bias0);
         x[mt][2] = fmaf(a0, x[mt][2], g0 * bias1);
@@ -567,8 +587,8 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       if (i + 2 < left) load_keys(st);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        t0 = fmaxf(t0, fmaxf(x[mt][0], x[mt][2]));
-        t1 = fmaxf(t1, fmaxf(x[mt][1], x[mt][3]));
+        t0 = fmax3(t0, x[mt][0], x[mt][2]);
+        t1 = fmax3(t1, x[mt][1], x[mt][3]);
       }
 
       // ---- running maxima of the logits and of the value scales' exponents
@@ -582,7 +602,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           if (dead[h] >> lane & 1u)
 #pragma unroll
             for (int g = 0; g < NG / 2; ++g)
-              sts_zero(ring_at + Ring::kValues + Ring::kCodes + (32 * h + lane) * (D / 16) + 4 * g);
+              *reinterpret_cast<uint32_t*>(smem + at0 + Ring::kValues + Ring::kCodes + (32 * h + lane) * (D / 16) + 4 * g) = 0;
         fence_proxy_async_smem();
         __syncwarp();
       }
@@ -594,8 +614,8 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          vs0[mt][b] = lds<2>(wbase + mt * D + 2 * SL * b) << 16;
-          vs1[mt][b] = lds<2>(wbase + mt * D + D / 2 + 2 * SL * b) << 16;
+          vs0[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + 2 * SL * b)) * shl16;
+          vs1[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + D / 2 + 2 * SL * b)) * shl16;
           vtop[b] = max(vtop[b], max(vs0[mt][b], vs1[mt][b]));
         }
       // The reference m and the unit of the weights move only when a logit passes m by
@@ -656,21 +676,21 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
             pf[1][b][1] = transpose8x8(f16x2(w10 - f16_lo(r1), w11 - f16_hi(r1)));
           }
         }
-        const uint32_t va = vbase + mt * 8 * D;
+        const uint8_t* va = smem + vbase + mt * 8 * D;
         uint32_t wa[NG / 2], wb[NG / 2], wc[NG / 2], wd[NG / 2];
-        lds_words(va, wa);
-        lds_words(va + vother, wb);
-        lds_words(va + 4 * D, wc);
-        lds_words(va + vother + 4 * D, wd);
+        words(va, wa);
+        words(va + vother, wb);
+        words(va + 4 * D, wc);
+        words(va + vother + 4 * D, wd);
 #pragma unroll
         for (int w = 0; w < NG / 2; ++w) {
           // low nibbles of two keys side by side, then the high ones: byte 2i + j holds
           // dimensions 2j (lo) or 2j + 1 (hi) of group 2w + i for both keys
           constexpr uint32_t M = 0x0f0f0f0fu;
           uint32_t loab[4], hiab[4], locd[4], hicd[4];
-          e2m1x8((wa[w] & M) | (wb[w] << 4 & ~M), loab);
+          e2m1x8((wa[w] & M) | (wb[w] * shl4 & ~M), loab);
           e2m1x8((wa[w] >> 4 & M) | (wb[w] & ~M), hiab);
-          e2m1x8((wc[w] & M) | (wd[w] << 4 & ~M), locd);
+          e2m1x8((wc[w] & M) | (wd[w] * shl4 & ~M), locd);
           e2m1x8((wc[w] >> 4 & M) | (wd[w] & ~M), hicd);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -770,7 +790,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4DecodeParams p, int ctas_max) {
   constexpr int kVals = 256, kHeads = kVals / D, kAhead = 6;
   extern __shared__ float s_w[];  // [CTAs][kHeads] weights
-  __shared__ int s_warp[8], s_find[3];
+  __shared__ int s_warp[8], s_find[5];
   __shared__ float s_top[kHeads], s_sum[kHeads];
   __shared__ float4 s_y[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hkv = p.c.hkv, vals = p.group * D;
@@ -785,7 +805,7 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4DecodeParams p, int 
     if (lane >= o) inc += up;
   }
   if (lane == 31) s_warp[warp] = inc;
-  if (tid == 0) s_find[0] = -1;
+  if (tid == 0) s_find[0] = s_find[1] = s_find[2] = s_find[3] = 0, s_find[4] = 1;
   __syncthreads();
   int base = inc - mine, total = 0;
 #pragma unroll
@@ -793,32 +813,44 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4DecodeParams p, int 
     if (w < warp) base += s_warp[w];
     total += s_warp[w];
   }
-  const int units = total * hkv, ctas = min(ctas_max, (units + kKv4MinUnits - 1) / kKv4MinUnits), cta = blockIdx.x;
+  const int cost = (2 * total + p.nreq) * hkv;
+  const int ctas = min(ctas_max, max(1, cost / kKv4MinCost)), cta = blockIdx.x;
   // a block leaves only after the main kernel: the next launch waits for this one alone
-  if (cta + 1 >= ctas) {
+  if (cta + 1 >= ctas || total == 0) {
     pdl_wait();
     return;
   }
-  const int each = units / ctas, more = units - each * ctas;
-  const int u0 = each * cta + min(cta, more), end = u0 + each + (cta < more ? 1 : 0);
-  // the request of the CTA's last unit
-  for (int r = rq0; r < rq1; ++r) {
-    const int n = (kv4_length(p, r) + kKv4Tile - 1) / kKv4Tile;
-    if (n && base * hkv < end && end <= (base + n) * hkv) {
-      s_find[0] = r;
-      s_find[1] = base;
-      s_find[2] = n;
-    }
-    base += n;
+  const int each = cost / ctas, more = cost - each * ctas;
+  const int x0 = each * cta + min(cta, more), x1 = x0 + each + (cta < more ? 1 : 0);
+  // tiles before this CTA's run and before the next one's
+  for (int r = rq0, b = base; r < rq1; ++r) {
+    const int n = (kv4_length(p, r) + kKv4Tile - 1) / kKv4Tile, seg = 2 * n + 1;
+    const int y0 = x0 - (2 * b + r) * hkv, y1 = x1 - (2 * b + r) * hkv;
+    if (y0 >= 0 && y0 < seg * hkv) s_find[0] = b * hkv + y0 / seg * n + kv4_tiles_before(y0 % seg, n);
+    if (y1 >= 0 && y1 < seg * hkv) s_find[1] = b * hkv + y1 / seg * n + kv4_tiles_before(y1 % seg, n);
+    b += n;
   }
   __syncthreads();
-  const int r = s_find[0], nt = s_find[2];
-  const int g = (end - 1 - s_find[1] * hkv) / nt, first = s_find[1] * hkv + g * nt, stop = first + nt;
-  if (first < u0 || stop <= end) {  // begun earlier, or finished here
+  const int u0 = s_find[0], end = s_find[1];
+  // the request of the CTA's last tile
+  for (int r = rq0, b = base; r < rq1; ++r) {
+    const int n = (kv4_length(p, r) + kKv4Tile - 1) / kKv4Tile;
+    if (n && b * hkv < end && end <= (b + n) * hkv) {
+      s_find[2] = r;
+      s_find[3] = b;
+      s_find[4] = n;
+    }
+    b += n;
+  }
+  __syncthreads();
+  const int r = s_find[2], nt = s_find[4];
+  const int g = u0 < end ? (end - 1 - s_find[3] * hkv) / nt : 0, first = s_find[3] * hkv + g * nt, stop = first + nt;
+  if (u0 == end || first < u0 || stop <= end) {  // no tiles, begun earlier, or finished here
     pdl_wait();
     return;
   }
-  const int last = stop - 1 < more * (each + 1) ? (stop - 1) / (each + 1) : more + (stop - 1 - more * (each + 1)) / each;
+  const int xl = (2 * s_find[3] + r) * hkv + g * (2 * nt + 1) + (nt == 1 ? 0 : 2 * nt - 1);  // where its last tile's cost begins
+  const int last = xl < more * (each + 1) ? xl / (each + 1) : more + (xl - more * (each + 1)) / each;
   const int parts = last - cta + 1, pf = kv4_piece_floats(p.group, D);
   const int v0 = blockIdx.y * kVals, h0 = v0 / D;  // this block's values and heads of the group
   // part 0: slot 1 of the CTA it begins in, then slot 0 of those after it

@@ -2057,8 +2057,8 @@ int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ld
   if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
   if (int64_t(max_pages) * cache->page_rows >= (int64_t(1) << 31))
     return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
-  // units of work are counted in 32 bits
-  if ((int64_t(max_pages) * cache->page_rows / tg::kKv4Tile + 1) * nreq >= (int64_t(1) << 31) / cache->hkv)
+  // the cost of the work is counted in 32 bits
+  if ((2 * (int64_t(max_pages) * cache->page_rows / tg::kKv4Tile + 1) + 1) * nreq >= (int64_t(1) << 31) / cache->hkv)
     return fail(TG_ERR_UNSUPPORTED, "nreq * max_pages * page_rows * hkv is too large");
   if (nreq == 0) return TG_OK;
   const int64_t width = int64_t(hq) * cache->head_dim;
