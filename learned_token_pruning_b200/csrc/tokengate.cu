@@ -1770,14 +1770,21 @@ int check_qk(int dtype, int64_t m, int32_t hq, int32_t hkv, int32_t head_dim, fl
   return TG_OK;
 }
 
-int qk_rope_bwd_blocks(int64_t m) {
-  return static_cast<int>(std::min<int64_t>((m + tg::kRopeWarps - 1) / tg::kRopeWarps, 2 * sm_count()));
+// Warps that share a row: one per pass while that is about a wave of the GPU (16 warps an SM),
+// where a row's passes one after the other are what takes time, else one.
+int qk_rope_split(int64_t m, int passes) { return m * passes <= 32 * int64_t(sm_count()) ? passes : 1; }
+
+int qk_rope_passes(int hq, int hkv, int head_dim) {
+  return head_dim == 128 ? tg::RopePasses<128>(hq, hkv).all : tg::RopePasses<64>(hq, hkv).all;
 }
+
+// blocks of the backward kernel at most (its workspace holds a partial of each)
+int qk_rope_bwd_blocks() { return 2 * sm_count(); }
 
 }  // namespace
 
 static size_t qk_rope_bwd_ws_bytes(int64_t m, int head_dim) {
-  return static_cast<size_t>(qk_rope_bwd_blocks(m)) * 2 * head_dim * sizeof(float);
+  return m > 0 ? static_cast<size_t>(qk_rope_bwd_blocks()) * 2 * head_dim * sizeof(float) : 0;
 }
 
 extern "C" {
@@ -1814,7 +1821,7 @@ int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int 
   p.k_out = k_out;
   p.ldqo = ldqo;
   p.ldko = ldko;
-  p.split = 1;
+  p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
   const dim3 grid(static_cast<unsigned>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps)), block(32 * tg::kRopeWarps);
   const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
   cudaStream_t st = as_stream(stream);
@@ -1874,7 +1881,9 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
   p.dq = dq;
   p.dk = dk;
   p.part = sums ? static_cast<float*>(ws) : nullptr;
-  const int blocks = qk_rope_bwd_blocks(m);
+  p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
+  const int blocks = static_cast<int>(
+      std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_bwd_blocks()));
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * tg::kRopeWarps);
   const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
   auto run = [&](auto kern) { return launch_pdl("k_qk_rope_bwd", kern, grid, block, 0, st, p, tab); };

@@ -385,63 +385,79 @@ def tg_pruned_prefill_layer_varlen(W: LayerWeights, S: LayerShape, hidden_kept, 
 # -----------------------------------------------------------------------------
 # Paged 4-bit cache, page tables, and the q/k norm + rotation on its own.  The
 # shapes the entry points cannot see (they get pointers) are checked here.
+# These calls are short on the device, so what they cost the host counts: types are
+# compared by identity, the device and the stream are asked for once a call.
 # -----------------------------------------------------------------------------
+_I32T, _F32T, _U8T = torch.int32, torch.float32, torch.uint8
+
+
 def _need(ok: bool, what: str):
     if not ok:
         raise TokenGateError("marshal", 1, what)
 
 
-def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: Optional[int] = None):
+def _here() -> int:
+    """The current CUDA device (-2, which no tensor has, where there is none)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _on(stream, dev: int) -> int:
+    """The cudaStream_t of `stream`, or of the current stream of the current device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, dev: int, numel: Optional[int] = None):
     """Address of a contiguous tensor of the current device, its type and size checked (None stays NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+    if t.dtype is not dtype or not t.is_contiguous() or (numel is not None and t.numel() != numel):
         raise TokenGateError("marshal", 1, f"{name} must be a contiguous {dtype} tensor"
                              + (f" of {numel} elements" if numel is not None else ""))
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise TokenGateError("marshal", 1, f"{name} is not on the current CUDA device")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, width: int):
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, rows: int, width: int):
     """(address, leading dimension) of a [rows, width] view with unit inner stride on the current device."""
-    if t.dim() != 2 or t.dtype != dtype or t.shape[0] != rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise TokenGateError("marshal", 1, f"{name} must be a {dtype} [{rows}, {width}] view with unit inner stride")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.dtype is not dtype or t.shape != (rows, width):
+        raise TokenGateError("marshal", 1, f"{name} must be a {dtype} [{rows}, {width}] view")
+    ld, inner = t.stride()
+    if inner != 1 and width > 1:
+        raise TokenGateError("marshal", 1, f"{name} must have unit inner stride")
+    if t.get_device() != dev:
         raise TokenGateError("marshal", 1, f"{name} is not on the current CUDA device")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else max(t.stride(0), width))
+    return t.data_ptr(), ld if rows > 1 else max(ld, width)
 
 
 def tg_page_tables(lens, new_rows, release, page_rows: int, tables, free_pages, n_free, lens_out, n_free_out, slots,
                    row_start, stream=None):
     """lens/new_rows/lens_out int32 [nreq], release uint8 [nreq] or None, tables int32 [nreq, max_pages], free_pages
     int32 [cap], n_free/n_free_out int32 [1], slots int32 [nslots], row_start int32 [nreq + 1]."""
-    n, i32 = lens.numel(), torch.int32
+    n, i32, dev = lens.numel(), _I32T, _here()
     _need(tables.dim() == 2 and tables.shape[0] == n, "tables must be [nreq, max_pages]")
-    rc = lib().tg_page_tables(_arg(lens, "lens", i32), _arg(new_rows, "new_rows", i32, n),
-                              _arg(release, "release", torch.uint8, n), n, int(page_rows), _arg(tables, "tables", i32),
-                              tables.shape[1], _arg(free_pages, "free_pages", i32), free_pages.numel(),
-                              _arg(n_free, "n_free", i32, 1), _arg(lens_out, "lens_out", i32, n),
-                              _arg(n_free_out, "n_free_out", i32, 1), _arg(slots, "slots", i32), slots.numel(),
-                              _arg(row_start, "row_start", i32, n + 1), _stream(stream))
+    rc = lib().tg_page_tables(_arg(lens, "lens", i32, dev), _arg(new_rows, "new_rows", i32, dev, n),
+                              _arg(release, "release", _U8T, dev, n), n, page_rows, _arg(tables, "tables", i32, dev),
+                              tables.shape[1], _arg(free_pages, "free_pages", i32, dev), free_pages.numel(),
+                              _arg(n_free, "n_free", i32, dev, 1), _arg(lens_out, "lens_out", i32, dev, n),
+                              _arg(n_free_out, "n_free_out", i32, dev, 1), _arg(slots, "slots", i32, dev), slots.numel(),
+                              _arg(row_start, "row_start", i32, dev, n + 1), _on(stream, dev))
     _check("tg_page_tables", rc)
 
 
 def tg_qk_norm_rope(q, k, head_dim: int, pos, w_q, w_k, norm_eps: float, rope_theta: float, q_out, k_out,
                     qk_norm: bool = True, stream=None):
     """q/k/q_out/k_out 2-D row views [m, heads*head_dim] (rows may be strided; q_out/k_out may be q/k); pos int32 [m]."""
-    m, dt = q.shape[0], q.dtype
-    _dtype(q)
-    _need(q.shape[1] % head_dim == 0 and k.shape[1] % head_dim == 0, "rows must hold whole heads")
-    qp, ldq = _rows(q, "q", dt, m, q.shape[1])
-    kp, ldk = _rows(k, "k", dt, m, k.shape[1])
-    qo, ldqo = _rows(q_out, "q_out", dt, m, q.shape[1])
-    ko, ldko = _rows(k_out, "k_out", dt, m, k.shape[1])
-    f32 = torch.float32
-    rc = lib().tg_qk_norm_rope(qp, ldq, kp, ldk, _dtype(q), m, q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim,
-                               _arg(pos, "pos", torch.int32, m), _arg(w_q, "w_q", f32, head_dim),
-                               _arg(w_k, "w_k", f32, head_dim), 1 if qk_norm else 0, float(norm_eps), float(rope_theta),
-                               qo, ldqo, ko, ldko, _stream(stream))
+    (m, wq), wk, dt, dev = q.shape, k.shape[1], q.dtype, _here()
+    _need(wq % head_dim == 0 and wk % head_dim == 0, "rows must hold whole heads")
+    qp, ldq = _rows(q, "q", dt, dev, m, wq)
+    kp, ldk = _rows(k, "k", dt, dev, m, wk)
+    qo, ldqo = _rows(q_out, "q_out", dt, dev, m, wq)
+    ko, ldko = _rows(k_out, "k_out", dt, dev, m, wk)
+    rc = lib().tg_qk_norm_rope(qp, ldq, kp, ldk, _dtype(q), m, wq // head_dim, wk // head_dim, head_dim,
+                               _arg(pos, "pos", _I32T, dev, m), _arg(w_q, "w_q", _F32T, dev, head_dim),
+                               _arg(w_k, "w_k", _F32T, dev, head_dim), 1 if qk_norm else 0, norm_eps, rope_theta,
+                               qo, ldqo, ko, ldko, _on(stream, dev))
     _check("tg_qk_norm_rope", rc)
 
 
@@ -453,20 +469,18 @@ def tg_qk_norm_rope_backward(q, k, head_dim: int, pos, w_q, w_k, norm_eps: float
                              ws, dw_q=None, dw_k=None, qk_norm: bool = True, stream=None):
     """q/k the forward's inputs; dq/dk fp32 [m, heads*head_dim] contiguous; dq_in/dk_in 2-D row views in q's type;
     ws a device byte buffer of qk_rope_backward_workspace_bytes(...) bytes (or None without dw_q and dw_k)."""
-    m, dt, f32 = q.shape[0], q.dtype, torch.float32
-    _dtype(q)
-    _need(q.shape[1] % head_dim == 0 and k.shape[1] % head_dim == 0, "rows must hold whole heads")
-    qp, ldq = _rows(q, "q", dt, m, q.shape[1])
-    kp, ldk = _rows(k, "k", dt, m, k.shape[1])
-    qo, ldqo = _rows(dq_in, "dq_in", dt, m, q.shape[1])
-    ko, ldko = _rows(dk_in, "dk_in", dt, m, k.shape[1])
+    (m, wq), wk, dt, f32, dev = q.shape, k.shape[1], q.dtype, _F32T, _here()
+    _need(wq % head_dim == 0 and wk % head_dim == 0, "rows must hold whole heads")
+    qp, ldq = _rows(q, "q", dt, dev, m, wq)
+    kp, ldk = _rows(k, "k", dt, dev, m, wk)
+    qo, ldqo = _rows(dq_in, "dq_in", dt, dev, m, wq)
+    ko, ldko = _rows(dk_in, "dk_in", dt, dev, m, wk)
     rc = lib().tg_qk_norm_rope_backward(
-        qp, ldq, kp, ldk, _dtype(q), m, q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim,
-        _arg(pos, "pos", torch.int32, m), _arg(w_q, "w_q", f32, head_dim), _arg(w_k, "w_k", f32, head_dim),
-        1 if qk_norm else 0, float(norm_eps), float(rope_theta), _arg(dq, "dq", f32, q.numel()),
-        _arg(dk, "dk", f32, k.numel()), qo, ldqo, ko, ldko, _arg(dw_q, "dw_q", f32, head_dim),
-        _arg(dw_k, "dw_k", f32, head_dim), _arg(ws, "ws", torch.uint8), ws.numel() if ws is not None else 0,
-        _stream(stream))
+        qp, ldq, kp, ldk, _dtype(q), m, wq // head_dim, wk // head_dim, head_dim, _arg(pos, "pos", _I32T, dev, m),
+        _arg(w_q, "w_q", f32, dev, head_dim), _arg(w_k, "w_k", f32, dev, head_dim), 1 if qk_norm else 0, norm_eps,
+        rope_theta, _arg(dq, "dq", f32, dev, m * wq), _arg(dk, "dk", f32, dev, m * wk), qo, ldqo, ko, ldko,
+        _arg(dw_q, "dw_q", f32, dev, head_dim), _arg(dw_k, "dw_k", f32, dev, head_dim), _arg(ws, "ws", _U8T, dev),
+        ws.numel() if ws is not None else 0, _on(stream, dev))
     _check("tg_qk_norm_rope_backward", rc)
 
 
@@ -481,12 +495,12 @@ class KV4Cache:
         n = pages * hkv * rows
         self.num_pages, self.hkv, self.page_rows, self.head_dim = pages, hkv, rows, 2 * half
         self.k_codes, self.v_codes, self.k_scales, self.v_scales, self.bias = k_codes, v_codes, k_scales, v_scales, bias
-        self.device = k_codes.get_device()
+        self.device, bf = _here(), torch.bfloat16
         self.struct = KV4CacheStruct(
-            _arg(k_codes, "k_codes", torch.uint8), _arg(v_codes, "v_codes", torch.uint8, n * half),
-            _arg(k_scales, "k_scales", torch.bfloat16, n * half // 16),
-            _arg(v_scales, "v_scales", torch.bfloat16, n * half // 16),
-            _arg(bias, "bias", torch.float32, pages * rows), pages, rows, hkv, 2 * half)
+            _arg(k_codes, "k_codes", _U8T, self.device), _arg(v_codes, "v_codes", _U8T, self.device, n * half),
+            _arg(k_scales, "k_scales", bf, self.device, n * half // 16),
+            _arg(v_scales, "v_scales", bf, self.device, n * half // 16),
+            _arg(bias, "bias", _F32T, self.device, pages * rows), pages, rows, hkv, 2 * half)
         self.ref = ctypes.byref(self.struct)
 
     @classmethod
@@ -497,28 +511,29 @@ class KV4Cache:
                    torch.zeros(num_pages, page_rows, device=device) if bias else None)
 
 
-def _on_cache(cache: KV4Cache):
-    _need(cache.device == torch.cuda.current_device(), "the cache is not on the current CUDA device")
+def _on_cache(cache: KV4Cache, dev: int):
+    if cache.device != dev:
+        raise TokenGateError("marshal", 1, "the cache is not on the current CUDA device")
     return cache.ref
 
 
 def tg_kv4_store(cache: KV4Cache, k, v, bias, slots, stream=None):
     """k/v 2-D row views [rows, hkv*head_dim]; bias fp32 [rows] or None; slots int32 [rows] (negative: left out)."""
-    n, w = k.shape[0], cache.hkv * cache.head_dim
-    kp, ldk = _rows(k, "k", k.dtype, n, w)
-    vp, ldv = _rows(v, "v", k.dtype, n, w)
-    rc = lib().tg_kv4_store(_on_cache(cache), kp, ldk, vp, ldv, _dtype(k), n, _arg(bias, "bias", torch.float32, n),
-                            _arg(slots, "slots", torch.int32, n), _stream(stream))
+    n, w, dt, dev = k.shape[0], cache.hkv * cache.head_dim, k.dtype, _here()
+    kp, ldk = _rows(k, "k", dt, dev, n, w)
+    vp, ldv = _rows(v, "v", dt, dev, n, w)
+    rc = lib().tg_kv4_store(_on_cache(cache, dev), kp, ldk, vp, ldv, _dtype(k), n, _arg(bias, "bias", _F32T, dev, n),
+                            _arg(slots, "slots", _I32T, dev, n), _on(stream, dev))
     _check("tg_kv4_store", rc)
 
 
 def tg_kv4_load(cache: KV4Cache, slots, k, v, bias=None, stream=None):
     """The values of the cache's rows into k/v (2-D row views [rows, hkv*head_dim]) and their biases."""
-    n, w = k.shape[0], cache.hkv * cache.head_dim
-    kp, ldk = _rows(k, "k", k.dtype, n, w)
-    vp, ldv = _rows(v, "v", k.dtype, n, w)
-    rc = lib().tg_kv4_load(_on_cache(cache), _arg(slots, "slots", torch.int32, n), n, kp, ldk, vp, ldv, _dtype(k),
-                           _arg(bias, "bias", torch.float32, n), _stream(stream))
+    n, w, dt, dev = k.shape[0], cache.hkv * cache.head_dim, k.dtype, _here()
+    kp, ldk = _rows(k, "k", dt, dev, n, w)
+    vp, ldv = _rows(v, "v", dt, dev, n, w)
+    rc = lib().tg_kv4_load(_on_cache(cache, dev), _arg(slots, "slots", _I32T, dev, n), n, kp, ldk, vp, ldv, _dtype(k),
+                           _arg(bias, "bias", _F32T, dev, n), _on(stream, dev))
     _check("tg_kv4_load", rc)
 
 
@@ -530,15 +545,16 @@ def tg_kv4_decode_attention(cache: KV4Cache, q, tables, lens, head_gain, head_te
                             lse=None, flags: int = 0, stream=None):
     """q/out 2-D row views [nreq, hq*head_dim]; tables int32 [nreq, max_pages]; lens int32 [nreq]; ratio fp32 [nreq]
     or None; lse fp32 [nreq, hq] or None; ws a device byte buffer of kv4_decode_workspace_bytes(...) bytes."""
-    n, i32, f32 = q.shape[0], torch.int32, torch.float32
-    _need(q.shape[1] % cache.head_dim == 0, "rows must hold whole heads")
+    (n, w), dt, i32, f32, dev = q.shape, q.dtype, _I32T, _F32T, _here()
+    _need(w % cache.head_dim == 0, "rows must hold whole heads")
     _need(tables.dim() == 2 and tables.shape[0] == n, "tables must be [nreq, max_pages]")
-    hq = q.shape[1] // cache.head_dim
-    qp, ldq = _rows(q, "q", q.dtype, n, q.shape[1])
-    op, ldo = _rows(out, "out", q.dtype, n, q.shape[1])
-    rc = lib().tg_kv4_decode_attention(_on_cache(cache), qp, ldq, _dtype(q), _arg(tables, "tables", i32), tables.shape[1],
-                                       _arg(lens, "lens", i32, n), n, hq, _arg(head_gain, "head_gain", f32, hq),
-                                       _arg(head_temp, "head_temp", f32, hq), _arg(ratio, "ratio", f32, n), float(sm_scale),
-                                       op, ldo, _arg(lse, "lse", f32, n * hq), _arg(ws, "ws", torch.uint8),
-                                       ws.numel() if ws is not None else 0, int(flags), _stream(stream))
+    hq = w // cache.head_dim
+    qp, ldq = _rows(q, "q", dt, dev, n, w)
+    op, ldo = _rows(out, "out", dt, dev, n, w)
+    rc = lib().tg_kv4_decode_attention(_on_cache(cache, dev), qp, ldq, _dtype(q), _arg(tables, "tables", i32, dev),
+                                       tables.shape[1], _arg(lens, "lens", i32, dev, n), n, hq,
+                                       _arg(head_gain, "head_gain", f32, dev, hq),
+                                       _arg(head_temp, "head_temp", f32, dev, hq), _arg(ratio, "ratio", f32, dev, n),
+                                       sm_scale, op, ldo, _arg(lse, "lse", f32, dev, n * hq), _arg(ws, "ws", _U8T, dev),
+                                       ws.numel() if ws is not None else 0, flags, _on(stream, dev))
     _check("tg_kv4_decode_attention", rc)
