@@ -13,6 +13,8 @@
 // reading 8 bytes of each of four neighbouring rows meets every bank once.
 #pragma once
 
+#include "attn_bwd_tc.cuh"
+#include "attn_tc.cuh"
 #include "common.cuh"
 
 namespace tg {
@@ -50,6 +52,7 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Cache& c, int32_t slot, int 
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 constexpr int kTabMaxReq = 4096;
+constexpr int kTabChunk = 256;
 constexpr int kTabPer = kTabMaxReq / kTabThreads;  // requests per thread at most
 
 struct PageTableParams {
@@ -202,19 +205,35 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
     const int first = (s_len[r] + p.page_rows - 1) / p.page_rows;
     p.tables[static_cast<int64_t>(r) * p.max_pages + first + (i - s_take[r])] = __ldcg(p.free_pages + (top - 1 - i));
   }
-  for (int i = t0; i < p.nslots; i += step) {
-    int32_t slot = -1;
-    if (i < nrows) {
-      const int r = find_request(s_rows, p.nreq, i);
-      const int32_t at = s_len[r] + (i - s_rows[r]);
-      const int32_t page = at / p.page_rows, held = (s_len[r] + p.page_rows - 1) / p.page_rows;
-      // pages taken in this call are read off the free list (another thread writes the table)
-      const int32_t id = page < held ? p.tables[static_cast<int64_t>(r) * p.max_pages + page]
-                                     : __ldcg(p.free_pages + (top - 1 - (s_take[r] + page - held)));
-      if (id < 0) raise_error(kErrPageTable, 4);
-      else slot = id * p.page_rows + (at - page * p.page_rows);
+  // 256 neighbouring slots to a warp: one search for the first row's request, then short
+  // walks, and the eight page ids a lane needs on their way together (129828 slots of
+  // 1000 requests: 33 us with a search for every slot)
+  const int lane = threadIdx.x & 31;
+  for (int c = t0 >> 5; c * kTabChunk < p.nslots; c += step >> 5) {
+    const int i0 = c * kTabChunk + lane;
+    int r = i0 < nrows ? find_request(s_rows, p.nreq, i0) : 0;
+    int32_t id[kTabChunk / 32], off[kTabChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kTabChunk / 32; ++k) {
+      const int i = i0 + 32 * k;
+      id[k] = -1;
+      off[k] = -1;
+      if (i < nrows) {
+        while (s_rows[r + 1] <= i) ++r;
+        const int32_t at = s_len[r] + (i - s_rows[r]);
+        const int32_t page = at / p.page_rows, held = (s_len[r] + p.page_rows - 1) / p.page_rows;
+        off[k] = at - page * p.page_rows;
+        // pages taken in this call are read off the free list (another thread writes the table)
+        id[k] = __ldcg(page < held ? p.tables + static_cast<int64_t>(r) * p.max_pages + page
+                                   : p.free_pages + (top - 1 - (s_take[r] + page - held)));
+      }
     }
-    p.slots[i] = slot;
+#pragma unroll
+    for (int k = 0; k < kTabChunk / 32; ++k) {
+      const int i = i0 + 32 * k;
+      if (id[k] < 0 && off[k] >= 0) raise_error(kErrPageTable, 4);
+      if (i < p.nslots) p.slots[i] = id[k] < 0 ? -1 : id[k] * p.page_rows + off[k];
+    }
   }
   for (int i = t0; i <= p.nreq; i += step) {
     p.row_start[i] = s_rows[i];
@@ -274,10 +293,63 @@ __device__ __forceinline__ uint32_t e2m1_code(float x, float s) {
   return c | (__float_as_uint(x) >> 28 & 8u);
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = c >> 1 & 3u, m = c & 1u;
-  const float v = e ? __uint_as_float((126u + e) << 23 | m << 22) : 0.5f * static_cast<float>(m);
-  return c & 8u ? -v : v;
+// Eight E2M1 codes, nearest with ties to the even code, +-6 at most; x[0] in the low nibble.
+__device__ __forceinline__ uint32_t e2m1_round8(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+      "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Eight codes of x / s, exactly the nearest ones; s > 0.
+//   bf16: x times the approximate 1 / s (1 ulp) is off by less than 2^-22 of itself, and a
+//   quotient of two bf16 numbers that is not a border between codes is 2^-11 of itself away
+//   from one (a border has 3 significant bits), so rounding the product to 15 bits puts
+//   quotients on a border exactly there and no other on the wrong side of one.
+//   fp32: the product is taken once a little below and once a little above; where the
+//   codes differ, a border lies between, and the comparisons decide.
+// Scales below 2^-100, whose reciprocals may not be floats, take the comparisons too.
+template <typename T>
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&x)[8], float s) {
+  float r, y[8], z[8];
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  uint32_t w, other;
+  if constexpr (sizeof(T) == 2) {
+    // y rounded to 15 bits as c - (c - y), c = (2^9 + 1) y: on the multiply-add pipe, in pairs
+    const uint64_t r2 = f2_pack(r, r), big = f2_pack(513.0f, 513.0f), minus = f2_pack(-1.0f, -1.0f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t v = f2_mul(f2_pack(x[2 * e], x[2 * e + 1]), r2), c = f2_mul(v, big);
+      f2_unpack(f2_fma(f2_fma(v, minus, c), minus, c), y[2 * e], y[2 * e + 1]);
+    }
+    w = other = e2m1_round8(y);
+  } else {
+    const float below = r * (1.0f - 9.5367431640625e-7f), above = r * (1.0f + 9.5367431640625e-7f);  // 2^-20
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e] * below, z[e] = x[e] * above;
+    w = e2m1_round8(y);
+    other = e2m1_round8(z);
+  }
+  if (w != other || s < 7.888609052210118e-31f) {  // 2^-100
+    w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= e2m1_code(x[e], s) << (4 * e);
+  }
+  return w;
+}
+
+// the values of the two codes in byte b of w
+template <int B>
+__device__ __forceinline__ float2 e2m1_values(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(h) : "r"(w >> (8 * B)));
+  float2 f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(h));
+  return f;
 }
 
 struct Kv4RowsParams {
@@ -297,90 +369,172 @@ __device__ __forceinline__ int kv4_word(int r, int gp, int32_t slot) {
   return D == 128 ? at ^ ((slot & 2) << 4) : at;
 }
 
-template <typename T, int D>
+// A thread takes the same eight values of K or V of one head (`li` of a row's) in IT rows: rows are
+// dealt to the blocks IT * per_block at a time, blockIdx.y counts 256 items of a row each.
+struct Kv4Place {
+  int li, head, l, g, l4;  // item of the row, head, eighth of the head, scale group, eighth of the group
+  bool is_v, mine;
+  int64_t row0;
+  int step;  // rows between this thread's
+  template <int D, int IT>
+  __device__ __forceinline__ static Kv4Place at(const Kv4RowsParams& p) {
+    Kv4Place t;
+    const int per_row = 2 * p.c.hkv * (D / 8), chunk = min(per_row, 256);
+    const int sub = threadIdx.x / chunk;
+    t.step = 256 / chunk;
+    t.li = threadIdx.x - sub * chunk + 256 * blockIdx.y;
+    t.mine = sub < t.step && t.li < per_row;  // eight neighbouring lanes alike: chunk and per_row are multiples of 16
+    t.row0 = static_cast<int64_t>(blockIdx.x) * IT * t.step + sub;
+    const int head2 = t.li / (D / 8);
+    t.l = t.li % (D / 8);
+    t.is_v = head2 >= p.c.hkv;
+    t.head = t.is_v ? head2 - p.c.hkv : head2;
+    t.g = t.l >> 2;
+    t.l4 = t.l & 3;
+    return t;
+  }
+};
+
+// The largest magnitude of a lane's eight values, as fp32 bits: infinities and NaN come out on top.
+__device__ __forceinline__ uint32_t top8(const uint4 (&w)[1]) {
+  const uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(w[0].x & m, w[0].y & m), __vmaxu2(w[0].z & m, w[0].w & m));  // a pair of bf16
+}
+__device__ __forceinline__ uint32_t top8(const uint4 (&w)[2]) {
+  const uint32_t m = 0x7fffffffu;
+  const uint32_t a = max(max(w[0].x & m, w[0].y & m), max(w[0].z & m, w[0].w & m));
+  return max(a, max(max(w[1].x & m, w[1].y & m), max(w[1].z & m, w[1].w & m)));
+}
+
+template <typename T, int D, int IT>
 __global__ void __launch_bounds__(256) k_kv4_store(const Kv4RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int L = D / 8;  // lanes per head row
-  const int per_row = 2 * p.c.hkv * L;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = i / per_row;
-  const bool in = row < p.rows;  // uniform over the eight lanes a shuffle reaches
-  const int li = static_cast<int>(i - row * per_row);
-  const int head2 = li / L, l = li % L, g = l >> 2, l4 = l & 3;
-  const bool is_v = head2 >= p.c.hkv;
-  const int head = is_v ? head2 - p.c.hkv : head2;
-  int32_t slot = in ? p.slots[row] : -1;
-  if (slot >= 0 && slot >= p.c.num_pages * p.c.page_rows) {
-    if (li == 0) raise_error(kErrKvSlot, 1);
-    slot = -1;
-  }
-  float x[8] = {};
-  if (slot >= 0)
-    load8(static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ldv : p.ldk) + head * D + l * 8, x);
-  // largest magnitude of the group as an integer: infinities and NaN come out on top
-  uint32_t top = 0;
+  const Kv4Place t = Kv4Place::at<D, IT>(p);
+  const T* src = static_cast<const T*>(t.is_v ? p.v : p.k) + t.head * D + t.l * 8;
+  const int64_t ld = t.is_v ? p.ldv : p.ldk;
+  uint8_t* codes = t.is_v ? p.c.v_codes : p.c.k_codes;
+  __nv_bfloat16* scales = (t.is_v ? p.c.v_scales : p.c.k_scales) + t.g;
+  const int64_t slots = p.c.num_pages * p.c.page_rows;
+  constexpr int kW = sizeof(T) / 2;
+  int32_t slot[IT];
+  uint4 raw[IT][kW];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // max / 6 in fp32, rounded to bf16: the second rounding meets no false tie
-  // (a quotient by 6 that is not a bf16 tie stays an fp32 step away from one)
-  const bool finite = top < 0x7f800000u;
-  const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? __uint_as_float(top) / 6.0f : __uint_as_float(0x7fffffffu));
-  const float s = __bfloat162float(sb);
-  uint32_t w = 0;  // eight codes, dimension 8l first
-  if (finite && s > 0.0f) {
+  for (int u = 0; u < IT; ++u) {
+    const int64_t row = t.row0 + u * t.step;
+    slot[u] = -1;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= e2m1_code(x[e], s) << (4 * e);
+    for (int i = 0; i < kW; ++i) raw[u][i] = make_uint4(0, 0, 0, 0);
+    if (t.mine && row < p.rows) {
+      slot[u] = p.slots[row];
+#pragma unroll
+      for (int i = 0; i < kW; ++i) raw[u][i] = reinterpret_cast<const uint4*>(src + row * ld)[i];
+    }
   }
-  // low half: unit (2 l4, g); high half: (2 l4 + 1, g).  The lane of the neighbouring
-  // group has the same units of group g ^ 1: each keeps one and hands over the other.
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, g & 1 ? w & 0xffffu : w >> 16, 4);
-  const uint32_t word = g & 1 ? got | (w & 0xffff0000u) : (w & 0xffffu) | got << 16;
-  if (slot < 0) return;
-  const int64_t at = kv4_row(p.c, slot, head);
-  const int r = 2 * l4 + (g & 1), gp = g >> 1;
-  uint8_t* codes = (is_v ? p.c.v_codes : p.c.k_codes) + at * (D / 2);
-  *reinterpret_cast<uint32_t*>(codes + kv4_word<D>(r, gp, slot)) = word;
-  if (l4 == 0) (is_v ? p.c.v_scales : p.c.k_scales)[at * (D / 32) + g] = sb;
-  if (li == 0 && p.c.bias) p.c.bias[slot] = p.bias ? p.bias[row] : 0.0f;
+#pragma unroll
+  for (int u = 0; u < IT; ++u) {
+    if (slot[u] >= slots) {
+      if (t.li == 0) raise_error(kErrKvSlot, 1);
+      slot[u] = -1;
+    }
+    // max / 6 rounded to bf16 by way of fp32, which meets no false tie: an fp32 quotient by 6
+    // that is not a bf16 tie stays an fp32 step away from one, and for a bf16 maximum the
+    // product with 1/6 (2^-25 off) is on a tie where the quotient is and 2^-12 away elsewhere
+    uint32_t top = top8(raw[u]);
+    float sixth;
+    if constexpr (kW == 1) {
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = max(top << 16, top & 0xffff0000u);
+      sixth = __uint_as_float(top) * (1.0f / 6.0f);
+    } else {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      sixth = __uint_as_float(top) / 6.0f;
+    }
+    const bool finite = top < 0x7f800000u;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? sixth : __uint_as_float(0x7fffffffu));
+    const float s = __bfloat162float(sb);
+    float x[8];
+    load8(reinterpret_cast<const T*>(raw[u]), x);
+    const uint32_t w = finite && s > 0.0f ? e2m1_codes8<T>(x, s) : 0u;  // dimension 8l first
+    // low half: unit (2 l4, g); high half: (2 l4 + 1, g).  The lane of the neighbouring
+    // group has the same units of group g ^ 1: each keeps one and hands over the other.
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, t.g & 1 ? w & 0xffffu : w >> 16, 4);
+    const uint32_t word = t.g & 1 ? got | (w & 0xffff0000u) : (w & 0xffffu) | got << 16;
+    if (slot[u] < 0) continue;
+    const int64_t at = kv4_row(p.c, slot[u], t.head);
+    *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + kv4_word<D>(2 * t.l4 + (t.g & 1), t.g >> 1, slot[u])) = word;
+    if (t.l4 == 0) scales[at * (D / 32)] = sb;
+    if (t.li == 0 && p.c.bias) p.c.bias[slot[u]] = p.bias ? p.bias[t.row0 + u * t.step] : 0.0f;
+  }
 }
 
-template <typename T, int D>
+template <typename T, int D, int IT>
 __global__ void __launch_bounds__(256) k_kv4_load(const Kv4RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int L = D / 8;
-  const int per_row = 2 * p.c.hkv * L;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = i / per_row;
-  const bool in = row < p.rows;
-  const int li = static_cast<int>(i - row * per_row);
-  const int head2 = li / L, l = li % L, g = l >> 2, l4 = l & 3;
-  const bool is_v = head2 >= p.c.hkv;
-  const int head = is_v ? head2 - p.c.hkv : head2;
-  int32_t slot = in ? p.slots[row] : -1;
-  if (slot >= 0 && slot >= p.c.num_pages * p.c.page_rows) {
-    if (li == 0) raise_error(kErrKvSlot, 2);
-    slot = -1;
-  }
-  const int64_t at = slot >= 0 ? kv4_row(p.c, slot, head) : 0;
-  const int r = 2 * l4 + (g & 1), gp = g >> 1;
-  uint32_t word = 0;
-  float s = 0.0f;
-  if (slot >= 0) {
-    word = *reinterpret_cast<const uint32_t*>((is_v ? p.c.v_codes : p.c.k_codes) + at * (D / 2) + kv4_word<D>(r, gp, slot));
-    s = __bfloat162float((is_v ? p.c.v_scales : p.c.k_scales)[at * (D / 32) + g]);
-  }
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, g & 1 ? word & 0xffffu : word >> 16, 4);
-  const uint32_t w = g & 1 ? got | (word & 0xffff0000u) : (word & 0xffffu) | got << 16;
-  if (slot < 0) return;
-  float x[8];
+  const Kv4Place t = Kv4Place::at<D, IT>(p);
+  T* dst = static_cast<T*>(const_cast<void*>(t.is_v ? p.v : p.k)) + t.head * D + t.l * 8;
+  const int64_t ld = t.is_v ? p.ldv : p.ldk;
+  const uint8_t* codes = t.is_v ? p.c.v_codes : p.c.k_codes;
+  const __nv_bfloat16* scales = (t.is_v ? p.c.v_scales : p.c.k_scales) + t.g;
+  const int64_t slots = p.c.num_pages * p.c.page_rows;
+  int32_t slot[IT];
+  uint32_t word[IT];
+  float s[IT];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = e2m1_value(w >> (4 * e) & 15u) * s;
-  store8(static_cast<T*>(const_cast<void*>(is_v ? p.v : p.k)) + row * (is_v ? p.ldv : p.ldk) + head * D + l * 8, x);
-  if (li == 0 && p.bias) p.bias[row] = p.c.bias ? p.c.bias[slot] : 0.0f;
+  for (int u = 0; u < IT; ++u) {
+    const int64_t row = t.row0 + u * t.step;
+    slot[u] = t.mine && row < p.rows ? p.slots[row] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < IT; ++u) {
+    if (slot[u] >= slots) {
+      if (t.li == 0) raise_error(kErrKvSlot, 2);
+      slot[u] = -1;
+    }
+    word[u] = 0;
+    s[u] = 0.0f;
+    if (slot[u] >= 0) {
+      const int64_t at = kv4_row(p.c, slot[u], t.head);
+      word[u] = *reinterpret_cast<const uint32_t*>(codes + at * (D / 2) + kv4_word<D>(2 * t.l4 + (t.g & 1), t.g >> 1, slot[u]));
+      s[u] = __bfloat162float(scales[at * (D / 32)]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < IT; ++u) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, t.g & 1 ? word[u] & 0xffffu : word[u] >> 16, 4);
+    const uint32_t w = t.g & 1 ? got | (word[u] & 0xffff0000u) : (word[u] & 0xffffu) | got << 16;
+    const int64_t row = t.row0 + u * t.step;
+    const float2 v[4] = {e2m1_values<0>(w), e2m1_values<1>(w), e2m1_values<2>(w), e2m1_values<3>(w)};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = v[e].x * s[u];
+      x[2 * e + 1] = v[e].y * s[u];
+    }
+    if constexpr (sizeof(T) == 4) {
+      // 32 bytes a lane: the lanes of a pair trade halves, so that one store writes whole sectors
+      const bool odd = t.l & 1;
+      float give[4], own[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        give[e] = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 4], 1);
+        own[e] = odd ? x[e + 4] : x[e];
+      }
+      if (slot[u] < 0) continue;
+      float* out = reinterpret_cast<float*>(dst + row * ld);
+      *reinterpret_cast<float4*>(out + (odd ? -4 : 0)) = odd ? make_float4(give[0], give[1], give[2], give[3])
+                                                             : make_float4(own[0], own[1], own[2], own[3]);
+      *reinterpret_cast<float4*>(out + (odd ? 4 : 8)) = odd ? make_float4(own[0], own[1], own[2], own[3])
+                                                            : make_float4(give[0], give[1], give[2], give[3]);
+    } else {
+      if (slot[u] < 0) continue;
+      store8(dst + row * ld, x);
+    }
+    if (t.li == 0 && p.bias) p.bias[row] = p.c.bias ? p.c.bias[slot[u]] : 0.0f;
+  }
 }
 
 }  // namespace tg

@@ -15,6 +15,8 @@
 // heads through shared memory.
 #pragma once
 
+#include "attn_bwd_tc.cuh"
+#include "attn_tc.cuh"
 #include "common.cuh"
 #include "kv4.cuh"
 #include "simt.cuh"
@@ -52,20 +54,29 @@ struct RopePasses {
       : of_q((hq + kHeads - 1) / kHeads), all(of_q + (hkv + kHeads - 1) / kHeads) {}
 };
 
-// cos and sin of the row's D/2 angles into the warp's table
+// A lane's frequencies, read once: an index that differs by lane is served from constant
+// memory one lane at a time.
 template <int D>
-__device__ __forceinline__ void rope_table(float2* cs, int32_t pos, const RopeTable& tab) {
-  const int lane = threadIdx.x & 31;
+struct RopeFreqs {
+  double f[D / 64];
+  __device__ __forceinline__ RopeFreqs(const RopeTable& tab) {
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) {
-    const double ang = static_cast<double>(pos) * tab.inv_freq[e * 32 + lane];
-    const double turns = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
-    const float red = static_cast<float>(fma(-turns, 6.283185307179586, ang));
-    float s, c;
-    sincosf(red, &s, &c);
-    cs[e * 32 + lane] = make_float2(c, s);
+    for (int e = 0; e < D / 64; ++e) f[e] = tab.inv_freq[e * 32 + (threadIdx.x & 31)];
   }
-}
+  // cos and sin of the row's D/2 angles into the warp's tables
+  __device__ __forceinline__ void table(float* cosines, float* sines, int32_t pos) const {
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      const double ang = static_cast<double>(pos) * f[e];
+      const double turns = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
+      const float red = static_cast<float>(fma(-turns, 6.283185307179586, ang));
+      float s, c;
+      sincosf(red, &s, &c);
+      cosines[e * 32 + (threadIdx.x & 31)] = c;
+      sines[e * 32 + (threadIdx.x & 31)] = s;
+    }
+  }
+};
 
 template <int D>
 __device__ __forceinline__ float head_sum(float v) {
@@ -86,228 +97,295 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const { load8(reinterpret_cast<const T*>(w), x); }
 };
 
-__device__ __forceinline__ void weights8(const float* w, float (&x)[8]) {
-  if (w) {
-    x[0] = w[0], x[1] = w[1], x[2] = w[2], x[3] = w[3], x[4] = w[4], x[5] = w[5], x[6] = w[6], x[7] = w[7];
-  } else {
+// Eight fp32 values as four register pairs: a packed operation does two of them.
+struct F8 {
+  uint64_t v[4];
+  __device__ __forceinline__ void get(const Raw8<__nv_bfloat16>& r) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 1.0f;
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(bf16_lo(w[i]), bf16_hi(w[i]));
   }
+  __device__ __forceinline__ void get(const Raw8<float>& r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = f2_pack(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+      v[2 * i + 1] = f2_pack(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+    }
+  }
+  __device__ __forceinline__ void from(const float* p) {  // 16-byte aligned
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = f2_pack(a.x, a.y), v[1] = f2_pack(a.z, a.w), v[2] = f2_pack(b.x, b.y), v[3] = f2_pack(b.z, b.w);
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(T* p) const {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(v[i], x[2 * i], x[2 * i + 1]);
+    store8(p, x);
+  }
+};
+// sum of x y over the head's lanes, both halves
+template <int D>
+__device__ __forceinline__ float head_dot(const F8& xa, const F8& ya, const F8& xb, const F8& yb) {
+  uint64_t s = f2_mul(xa.v[0], ya.v[0]), t = f2_mul(xb.v[0], yb.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    s = f2_fma(xa.v[i], ya.v[i], s);
+    t = f2_fma(xb.v[i], yb.v[i], t);
+  }
+  float lo, hi;
+  f2_unpack(f2_add(s, t), lo, hi);
+  return head_sum<D>(lo + hi);
 }
 
-// The first loads of a row are on their way while its angles are formed, and as many passes
-// as registers allow at a time, since a pass alone keeps 1 KB of a warp's loads in flight.
+template <int D>
+__device__ __forceinline__ void norm_weights(const QkRopeParams& p, float (*s_w)[D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * kRopeWarps) {
+    const float* w = i < D ? p.wq : p.wk;
+    s_w[i / D][i % D] = w && p.qk_norm ? w[i % D] : 1.0f;
+  }
+  __syncthreads();
+}
+
+// A warp's walk over its passes: its items (rows, or single passes where a row is shared) stride
+// through the launch; `step` passes are taken at a time.
+struct RopeWalk {
+  int64_t item, items, stride, row;
+  int pass, end, split, all;
+  __device__ __forceinline__ RopeWalk(const QkRopeParams& p, int all_)
+      : item(static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5)), items(p.m * p.split),
+        stride(static_cast<int64_t>(gridDim.x) * kRopeWarps), split(p.split), all(all_) {
+    place();
+  }
+  __device__ __forceinline__ void place() {
+    if (split == 1) {
+      row = item;
+      pass = 0;
+      end = all;
+    } else {  // few items then: 32 bits
+      row = static_cast<uint32_t>(item) / static_cast<uint32_t>(split);
+      pass = static_cast<int>(item - row * split);
+      end = pass + 1;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return item < items; }
+  __device__ __forceinline__ void next(int step) {
+    pass += step;
+    if (pass >= end) {
+      item += stride;
+      place();
+    }
+  }
+};
+
+// The next passes' loads, and the next row's position, are on their way while these are worked on.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRopeWarps, 2) k_qk_rope_fwd(const QkRopeParams p,
                                                                     const __grid_constant__ RopeTable tab) {
-  constexpr int LH = RopePasses<D>::kLanes, HW = RopePasses<D>::kHeads, CH = sizeof(T) == 2 ? 3 : 2;
-  __shared__ float2 s_cs[kRopeWarps][D / 2];
+  constexpr int LH = RopePasses<D>::kLanes, HW = RopePasses<D>::kHeads, CH = sizeof(T) == 2 ? 2 : 1;
+  __shared__ __align__(16) float s_c[kRopeWarps][D / 2], s_s[kRopeWarps][D / 2];
+  __shared__ __align__(16) float s_w[2][D];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LH, sub = lane / LH;
   const RopePasses<D> passes(p.hq, p.hkv);
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp, row = item / p.split;
-  if (row >= p.m) return;  // warp-uniform
-  const int step = p.split == 1 ? 1 : passes.all;
-  const int32_t pos = p.pos[row];
-  const T* q = static_cast<const T*>(p.q) + row * p.ldq + 8 * j;
-  const T* k = static_cast<const T*>(p.k) + row * p.ldk + 8 * j;
-  T* qo = static_cast<T*>(p.q_out) + row * p.ldqo + 8 * j;
-  T* ko = static_cast<T*>(p.k_out) + row * p.ldko + 8 * j;
-  float c[8], s[8], wa[8], wb[8];
-  bool angles = false;
-  int weights = -1;  // whose weights are loaded: 0 q, 1 k
-  for (int i0 = static_cast<int>(item - row * p.split); i0 < passes.all; i0 += CH * step) {
-    Raw8<T> xa[CH], xb[CH];
+  const RopeFreqs<D> freqs(tab);
+  norm_weights<D>(p, s_w);
+  RopeWalk ahead(p, passes.all), here(p, passes.all);
+  Raw8<T> xa[CH], xb[CH];
+  int32_t pos = 0;
+  auto load = [&]() {
+    const T* q = static_cast<const T*>(p.q) + ahead.row * p.ldq + sub * D + 8 * j;
+    const T* k = static_cast<const T*>(p.k) + ahead.row * p.ldk + sub * D + 8 * j;
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
-      const int i = i0 + u * step;
+      const int i = ahead.pass + u;
       const bool isk = i >= passes.of_q;
-      const int h = (isk ? i - passes.of_q : i) * HW + sub;
-      xa[u].zero();
-      xb[u].zero();
-      if (i < passes.all && h < (isk ? p.hkv : p.hq)) {
-        const T* x = (isk ? k : q) + static_cast<int64_t>(h) * D;
+      const int h0 = (isk ? i - passes.of_q : i) * HW;
+      if (i < ahead.end && h0 + sub < (isk ? p.hkv : p.hq)) {
+        const T* x = (isk ? k : q) + h0 * D;
         xa[u].load(x);
         xb[u].load(x + D / 2);
       }
     }
-    if (!angles) {
-      angles = true;
-      rope_table<D>(s_cs[warp], pos, tab);
-      __syncwarp();
+    pos = p.pos[ahead.row];
+  };
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 v = s_cs[warp][8 * j + e];
-        c[e] = v.x;
-        s[e] = v.y;
-      }
+  for (int u = 0; u < CH; ++u) xa[u].zero(), xb[u].zero();
+  if (ahead.more()) load();
+  F8 c, s, ns;
+  int64_t angles_of = -1;
+  while (here.more()) {
+    Raw8<T> ca[CH], cb[CH];
+#pragma unroll
+    for (int u = 0; u < CH; ++u) ca[u] = xa[u], cb[u] = xb[u];
+    if (angles_of != here.row) {
+      angles_of = here.row;
+      __syncwarp();
+      freqs.table(s_c[warp], s_s[warp], pos);
+      __syncwarp();
+      c.from(&s_c[warp][8 * j]);
+      s.from(&s_s[warp][8 * j]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ns.v[e] = s.v[e] ^ 0x8000000080000000ull;
     }
+    ahead.next(CH);
+    if (ahead.more()) load();
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
-      const int i = i0 + u * step;
-      if (i >= passes.all) break;
+      const int i = here.pass + u;
+      if (i >= here.end) break;
       const bool isk = i >= passes.of_q;
       const int h = (isk ? i - passes.of_q : i) * HW + sub;
-      float a[8], b[8];
-      xa[u].get(a);
-      xb[u].get(b);
+      F8 a, b, wa, wb;
+      a.get(ca[u]);
+      b.get(cb[u]);
       if (p.qk_norm) {
-        if (weights != isk) {
-          weights = isk;
-          const float* w = isk ? p.wk : p.wq;
-          weights8(w ? w + 8 * j : nullptr, wa);
-          weights8(w ? w + D / 2 + 8 * j : nullptr, wb);
-        }
-        float ss = 0.0f;
+        const float n = rsqrtf(head_dot<D>(a, a, b, b) * (1.0f / D) + p.eps);  // 2 ulp
+        const uint64_t n2 = f2_pack(n, n);
+        wa.from(&s_w[isk][8 * j]);
+        wb.from(&s_w[isk][D / 2 + 8 * j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-        const float r = 1.0f / sqrtf(head_sum<D>(ss) / static_cast<float>(D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] *= r * wa[e];
-          b[e] *= r * wb[e];
+        for (int e = 0; e < 4; ++e) {
+          a.v[e] = f2_mul(a.v[e], f2_mul(wa.v[e], n2));
+          b.v[e] = f2_mul(b.v[e], f2_mul(wb.v[e], n2));
         }
       }
       if (h < (isk ? p.hkv : p.hq)) {
-        float ya[8], yb[8];
+        T* y = (isk ? static_cast<T*>(p.k_out) + here.row * p.ldko : static_cast<T*>(p.q_out) + here.row * p.ldqo) +
+               h * D + 8 * j;
+        F8 ya, yb;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ya[e] = a[e] * c[e] - b[e] * s[e];
-          yb[e] = b[e] * c[e] + a[e] * s[e];
+        for (int e = 0; e < 4; ++e) {
+          ya.v[e] = f2_fma(b.v[e], ns.v[e], f2_mul(a.v[e], c.v[e]));
+          yb.v[e] = f2_fma(a.v[e], s.v[e], f2_mul(b.v[e], c.v[e]));
         }
-        T* y = (isk ? ko : qo) + static_cast<int64_t>(h) * D;
-        store8(y, ya);
-        store8(y + D / 2, yb);
+        ya.put(y);
+        yb.put(y + D / 2);
       }
     }
+    here.next(CH);
   }
 }
 
-// Gradients: the warps stride over the rows (or, for few rows, over their passes) and keep
-// their lanes' share of both norm-weight gradients in registers over all of them; the next
-// pass is loaded before the current one is worked on.  The block adds its warps' shares in
-// warp order, k_qk_rope_bwd_final the blocks' in block order, so reruns are bit-identical.
+// Gradients.  The lanes' share of both norm-weight gradients stays in registers over all of a
+// warp's passes; the block adds its warps' shares in warp order, k_qk_rope_bwd_final the
+// blocks' in block order, so reruns are bit-identical.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRopeWarps, 2) k_qk_rope_bwd(const QkRopeParams p,
                                                                     const __grid_constant__ RopeTable tab) {
   constexpr int LH = RopePasses<D>::kLanes, HW = RopePasses<D>::kHeads;
-  __shared__ float2 s_cs[kRopeWarps][D / 2];
+  __shared__ __align__(16) float s_c[kRopeWarps][D / 2], s_s[kRopeWarps][D / 2];
   __shared__ float s_dw[kRopeWarps][2 * D];
   __shared__ __align__(16) float s_w[2][D];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LH, sub = lane / LH;
   const RopePasses<D> passes(p.hq, p.hkv);
-  for (int i = threadIdx.x; i < 2 * D; i += 32 * kRopeWarps) {
-    const float* w = i < D ? p.wq : p.wk;
-    s_w[i / D][i % D] = w && p.qk_norm ? w[i % D] : 1.0f;
-  }
-  __syncthreads();
-  float dwa[2][8] = {}, dwb[2][8] = {};  // [q, k][dimension]
-  const int each = p.split == 1 ? passes.all : 1;  // passes of an item
-  const int64_t items = p.m * p.split, stride = static_cast<int64_t>(gridDim.x) * kRopeWarps;
+  const RopeFreqs<D> freqs(tab);
+  norm_weights<D>(p, s_w);
+  RopeWalk ahead(p, passes.all), here(p, passes.all);
+  F8 dwa[2], dwb[2];  // [q, k]
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dwa[0].v[e] = dwa[1].v[e] = dwb[0].v[e] = dwb[1].v[e] = 0;
   Raw8<T> xa, xb;
   Raw8<float> ya, yb;
-  // pass i of a row: its place, and its loads
-  auto load = [&](int64_t row, int i) {
-    const bool isk = i >= passes.of_q;
-    const int h = (isk ? i - passes.of_q : i) * HW + sub, heads = isk ? p.hkv : p.hq;
+  int32_t pos = 0;
+  auto load = [&]() {  // heads past the last are loaded as zeros: they add nothing to the sums
+    const bool isk = ahead.pass >= passes.of_q;
+    const int h = (isk ? ahead.pass - passes.of_q : ahead.pass) * HW + sub, heads = isk ? p.hkv : p.hq;
     xa.zero(), xb.zero(), ya.zero(), yb.zero();
     if (h < heads) {
-      const float* dy = (isk ? p.dk : p.dq) + (row * heads + h) * D + 8 * j;
+      const float* dy = (isk ? p.dk : p.dq) + (ahead.row * heads + h) * D + 8 * j;
       ya.load(dy);
       yb.load(dy + D / 2);
       if (p.qk_norm) {
-        const T* x = (isk ? static_cast<const T*>(p.k) + row * p.ldk : static_cast<const T*>(p.q) + row * p.ldq) +
-                     static_cast<int64_t>(h) * D + 8 * j;
+        const T* x = (isk ? static_cast<const T*>(p.k) + ahead.row * p.ldk : static_cast<const T*>(p.q) + ahead.row * p.ldq) +
+                     h * D + 8 * j;
         xa.load(x);
         xb.load(x + D / 2);
       }
     }
+    pos = p.pos[ahead.row];
   };
-  int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
-  if (item < items) load(item / p.split, static_cast<int>(item % p.split));
-  for (; item < items; item += stride) {
-    const int64_t row = item / p.split;
-    const int first = static_cast<int>(item - row * p.split);
-    __syncwarp();
-    rope_table<D>(s_cs[warp], p.pos[row], tab);
-    __syncwarp();
-    for (int i = first; i < first + each; ++i) {
-      const bool isk = i >= passes.of_q;
-      const int h = (isk ? i - passes.of_q : i) * HW + sub;
-      const Raw8<T> cxa = xa, cxb = xb;
-      const Raw8<float> cya = ya, cyb = yb;
-      if (i + 1 < first + each) load(row, i + 1);
-      else if (item + stride < items) load((item + stride) / p.split, static_cast<int>((item + stride) % p.split));
-      float a[8], b[8], ga[8], gb[8];
-      cya.get(a);
-      cyb.get(b);
+  if (ahead.more()) load();
+  int64_t angles_of = -1;
+  while (here.more()) {
+    const Raw8<T> cxa = xa, cxb = xb;
+    const Raw8<float> cya = ya, cyb = yb;
+    if (angles_of != here.row) {
+      angles_of = here.row;
+      __syncwarp();
+      freqs.table(s_c[warp], s_s[warp], pos);
+      __syncwarp();
+    }
+    ahead.next(1);
+    if (ahead.more()) load();
+    const bool isk = here.pass >= passes.of_q;
+    const int h = (isk ? here.pass - passes.of_q : here.pass) * HW + sub;
+    F8 a, b, ga, gb, c, s;
+    a.get(cya);
+    b.get(cyb);
+    c.from(&s_c[warp][8 * j]);
+    s.from(&s_s[warp][8 * j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 cs = s_cs[warp][8 * j + e];
-        ga[e] = a[e] * cs.x + b[e] * cs.y;
-        gb[e] = b[e] * cs.x - a[e] * cs.y;
-      }
-      if (p.qk_norm) {
-        cxa.get(a);
-        cxb.get(b);
-        float ss = 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      ga.v[e] = f2_fma(b.v[e], s.v[e], f2_mul(a.v[e], c.v[e]));
+      gb.v[e] = f2_fma(a.v[e], s.v[e] ^ 0x8000000080000000ull, f2_mul(b.v[e], c.v[e]));
+    }
+    if (p.qk_norm) {
+      a.get(cxa);
+      b.get(cxb);
+      const float n = rsqrtf(head_dot<D>(a, a, b, b) * (1.0f / D) + p.eps);  // 2 ulp
+      const uint64_t n2 = f2_pack(n, n);
+      auto take = [&](F8& da, F8& db) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-        const float r = 1.0f / sqrtf(head_sum<D>(ss) / static_cast<float>(D) + p.eps);
-        float wa[8], wb[8], dot = 0.0f;
-        load8(&s_w[isk][8 * j], wa);
-        load8(&s_w[isk][D / 2 + 8 * j], wb);
-        auto take = [&](float (&da)[8], float (&db)[8]) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            da[e] += ga[e] * a[e] * r;
-            db[e] += gb[e] * b[e] * r;
-          }
-        };
-        if (isk) take(dwa[1], dwb[1]);  // warp-uniform
-        else take(dwa[0], dwb[0]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ga[e] *= wa[e];
-          gb[e] *= wb[e];
-          dot += ga[e] * a[e] + gb[e] * b[e];
+        for (int e = 0; e < 4; ++e) {
+          da.v[e] = f2_fma(f2_mul(ga.v[e], n2), a.v[e], da.v[e]);
+          db.v[e] = f2_fma(f2_mul(gb.v[e], n2), b.v[e], db.v[e]);
         }
-        const float t = head_sum<D>(dot) / static_cast<float>(D) * r * r;
+      };
+      if (isk) take(dwa[1], dwb[1]);  // warp-uniform
+      else take(dwa[0], dwb[0]);
+      c.from(&s_w[isk][8 * j]);
+      s.from(&s_w[isk][D / 2 + 8 * j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ga[e] = r * (ga[e] - a[e] * t);
-          gb[e] = r * (gb[e] - b[e] * t);
-        }
+      for (int e = 0; e < 4; ++e) {
+        ga.v[e] = f2_mul(ga.v[e], c.v[e]);
+        gb.v[e] = f2_mul(gb.v[e], s.v[e]);
       }
-      if (h < (isk ? p.hkv : p.hq)) {
-        T* dx = (isk ? static_cast<T*>(p.k_out) + row * p.ldko : static_cast<T*>(p.q_out) + row * p.ldqo) +
-                static_cast<int64_t>(h) * D + 8 * j;
-        store8(dx, ga);
-        store8(dx + D / 2, gb);
+      const float t = -head_dot<D>(ga, a, gb, b) * (1.0f / D) * n * n;
+      const uint64_t t2 = f2_pack(t, t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ga.v[e] = f2_mul(n2, f2_fma(a.v[e], t2, ga.v[e]));
+        gb.v[e] = f2_mul(n2, f2_fma(b.v[e], t2, gb.v[e]));
       }
     }
+    if (h < (isk ? p.hkv : p.hq)) {
+      T* dx = (isk ? static_cast<T*>(p.k_out) + here.row * p.ldko : static_cast<T*>(p.q_out) + here.row * p.ldqo) +
+              h * D + 8 * j;
+      ga.put(dx);
+      gb.put(dx + D / 2);
+    }
+    here.next(1);
   }
   if (!p.part) return;
   // the warp's heads, then the block's warps
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a = dwa[t][e], b = dwb[t][e];
+    for (int e = 0; e < 4; ++e) {
+      float v[4];
+      f2_unpack(dwa[t].v[e], v[0], v[1]);
+      f2_unpack(dwb[t].v[e], v[2], v[3]);
 #pragma unroll
-      for (int o = LH; o < 32; o <<= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
-      if (sub == 0) {
-        s_dw[warp][t * D + 8 * j + e] = a;
-        s_dw[warp][t * D + D / 2 + 8 * j + e] = b;
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = LH; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (sub == 0) s_dw[warp][t * D + (i >> 1) * (D / 2) + 8 * j + 2 * e + (i & 1)] = v[i];
       }
     }
   __syncthreads();
@@ -319,19 +397,27 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2) k_qk_rope_bwd(const QkRope
   }
 }
 
-// dw_q, dw_k [D] from the blocks' partials; one block of 4 * D threads per tensor:
-// thread (c, d) adds the blocks b = c mod 4 in order, then the four sums are added.
-__global__ void __launch_bounds__(512) k_qk_rope_bwd_final(const float* part, int blocks, int d, float* dwq, float* dwk) {
-  __shared__ float s_sum[512];
+// dw_q, dw_k [D] from the blocks' partials: a block takes 32 dimensions of one of them, warp w
+// adds the blocks b = w mod 32 in order, and the 32 sums are added in order.
+__global__ void __launch_bounds__(1024) k_qk_rope_bwd_final(const float* part, int blocks, int d, float* dwq,
+                                                            float* dwk) {
+  __shared__ float s_sum[32][33];
   pdl_wait();
   pdl_launch_dependents();
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.y * 32 + lane;
   float* out = blockIdx.x ? dwk : dwq;
-  const int c = threadIdx.x / d, i = threadIdx.x % d;
+  const float* p = part + static_cast<int64_t>(blockIdx.x) * d + i;
   float v = 0.0f;
-  for (int b = c; b < blocks; b += 4) v += part[(static_cast<int64_t>(b) * 2 + blockIdx.x) * d + i];
-  s_sum[threadIdx.x] = v;
+#pragma unroll 10
+  for (int b = w; b < blocks; b += 32) v += p[static_cast<int64_t>(b) * 2 * d];
+  s_sum[w][lane] = v;
   __syncthreads();
-  if (c == 0 && out) out[i] = (s_sum[i] + s_sum[d + i]) + (s_sum[2 * d + i] + s_sum[3 * d + i]);
+  if (w == 0 && out) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += s_sum[k][lane];
+    out[i] = t;
+  }
 }
 
 }  // namespace tg

@@ -1778,13 +1778,13 @@ int qk_rope_passes(int hq, int hkv, int head_dim) {
   return head_dim == 128 ? tg::RopePasses<128>(hq, hkv).all : tg::RopePasses<64>(hq, hkv).all;
 }
 
-// blocks of the backward kernel at most (its workspace holds a partial of each)
-int qk_rope_bwd_blocks() { return 2 * sm_count(); }
+// blocks of either kernel at most: two an SM (the backward's workspace holds a partial of each)
+int qk_rope_blocks() { return 2 * sm_count(); }
 
 }  // namespace
 
 static size_t qk_rope_bwd_ws_bytes(int64_t m, int head_dim) {
-  return m > 0 ? static_cast<size_t>(qk_rope_bwd_blocks()) * 2 * head_dim * sizeof(float) : 0;
+  return m > 0 ? static_cast<size_t>(qk_rope_blocks()) * 2 * head_dim * sizeof(float) : 0;
 }
 
 extern "C" {
@@ -1822,7 +1822,8 @@ int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int 
   p.ldqo = ldqo;
   p.ldko = ldko;
   p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
-  const dim3 grid(static_cast<unsigned>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps)), block(32 * tg::kRopeWarps);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_blocks())));
+  const dim3 block(32 * tg::kRopeWarps);
   const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
   cudaStream_t st = as_stream(stream);
   auto run = [&](auto kern) { return launch_pdl("k_qk_rope_fwd", kern, grid, block, 0, st, p, tab); };
@@ -1883,7 +1884,7 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
   p.part = sums ? static_cast<float*>(ws) : nullptr;
   p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
   const int blocks = static_cast<int>(
-      std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_bwd_blocks()));
+      std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_blocks()));
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * tg::kRopeWarps);
   const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
   auto run = [&](auto kern) { return launch_pdl("k_qk_rope_bwd", kern, grid, block, 0, st, p, tab); };
@@ -1892,7 +1893,7 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
   else
     rc = head_dim == 128 ? run(tg::k_qk_rope_bwd<float, 128>) : run(tg::k_qk_rope_bwd<float, 64>);
   if (rc || !sums) return rc;
-  return launch_pdl("k_qk_rope_bwd_final", tg::k_qk_rope_bwd_final, dim3(2), dim3(4 * head_dim), 0, st,
+  return launch_pdl("k_qk_rope_bwd_final", tg::k_qk_rope_bwd_final, dim3(2, head_dim / 32), dim3(1024), 0, st,
                     static_cast<const float*>(p.part), blocks, int(head_dim), dw_q, dw_k);
 }
 
@@ -1988,8 +1989,7 @@ int kv4_rows(const char* what, bool load, const tg_kv4_cache* cache, const void*
   const int64_t width = int64_t(cache->hkv) * cache->head_dim;
   if ((rc = check_strided("k", k, ldk, width, es)) || (rc = check_strided("v", v, ldv, width, es))) return rc;
   if (!slots) return fail(TG_ERR_INVALID_ARG, "slots is null");
-  const int64_t blocks = (rows * (width / 4) + 255) / 256;  // one thread per eight K or V values
-  if (rows >= (int64_t(1) << 31) || blocks >= (int64_t(1) << 31)) return fail(TG_ERR_UNSUPPORTED, "too many rows");
+  if (rows >= (int64_t(1) << 31)) return fail(TG_ERR_UNSUPPORTED, "too many rows");
   p.k = k;
   p.v = v;
   p.ldk = ldk;
@@ -1997,13 +1997,31 @@ int kv4_rows(const char* what, bool load, const tg_kv4_cache* cache, const void*
   p.bias = const_cast<float*>(bias);
   p.slots = slots;
   p.rows = rows;
-  auto run = [&](auto kern) { return launch_pdl(what, kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p); };
+  // items of eight K or V values: a block takes 256 of a row, or as many whole rows, several
+  // times over where that fills the GPU.  8256 rows x 8 heads of 128, bf16: the loads of
+  // four rows under way together, 13.9 us into the cache, of one 18.1; out of it (fp32)
+  // two 17.9 us, one 18.9, four 22.7.  33 rows x 2 heads of 64, in and out: one
+  // 3.4 us, four 7.0
+  const int64_t per_row = width / 4, per_block = per_row < 256 ? 256 / per_row : 1, chunks = (per_row + 255) / 256;
+  if (chunks > 65535) return fail(TG_ERR_UNSUPPORTED, "hkv * head_dim is too large");
+  auto run = [&](auto several, auto one) {
+    const int64_t it = load ? 2 : 4;
+    const bool many = rows / (it * per_block) * chunks >= 2 * sm_count();
+    const int64_t rows_per = per_block * (many ? it : 1);
+    const dim3 grid(static_cast<unsigned>((rows + rows_per - 1) / rows_per), static_cast<unsigned>(chunks));
+    return launch_pdl(what, many ? several : one, grid, dim3(256), 0, st, p);
+  };
+  using bf16 = __nv_bfloat16;
   const bool bf = dtype == TG_BF16, wide = cache->head_dim == 128;
   if (load)
-    return bf ? (wide ? run(tg::k_kv4_load<__nv_bfloat16, 128>) : run(tg::k_kv4_load<__nv_bfloat16, 64>))
-              : (wide ? run(tg::k_kv4_load<float, 128>) : run(tg::k_kv4_load<float, 64>));
-  return bf ? (wide ? run(tg::k_kv4_store<__nv_bfloat16, 128>) : run(tg::k_kv4_store<__nv_bfloat16, 64>))
-            : (wide ? run(tg::k_kv4_store<float, 128>) : run(tg::k_kv4_store<float, 64>));
+    return bf ? (wide ? run(tg::k_kv4_load<bf16, 128, 2>, tg::k_kv4_load<bf16, 128, 1>)
+                      : run(tg::k_kv4_load<bf16, 64, 2>, tg::k_kv4_load<bf16, 64, 1>))
+              : (wide ? run(tg::k_kv4_load<float, 128, 2>, tg::k_kv4_load<float, 128, 1>)
+                      : run(tg::k_kv4_load<float, 64, 2>, tg::k_kv4_load<float, 64, 1>));
+  return bf ? (wide ? run(tg::k_kv4_store<bf16, 128, 4>, tg::k_kv4_store<bf16, 128, 1>)
+                    : run(tg::k_kv4_store<bf16, 64, 4>, tg::k_kv4_store<bf16, 64, 1>))
+            : (wide ? run(tg::k_kv4_store<float, 128, 4>, tg::k_kv4_store<float, 128, 1>)
+                    : run(tg::k_kv4_store<float, 64, 4>, tg::k_kv4_store<float, 64, 1>));
 }
 
 }  // namespace

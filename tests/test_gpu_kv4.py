@@ -205,6 +205,37 @@ def test_store_and_load_are_exact(rows, hkv, d, page, dtype):
     assert tg.tg_check_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top", [6.0, 1.0, 5.34375, 0.0703125, 3.0e38, 7e-31, 3e-38, 2.0 ** -128])
+def test_store_every_value_below_a_largest_one(dtype, top):
+    # the bf16 values from top down over eight powers of two, their neighbours in fp32, and the borders
+    # themselves: every code is the exact nearest, ties to even
+    top = synth.round_to(np.float32([top]), "bf16")[0]
+    bits = np.float32(top).view(np.uint32) >> 16
+    x = (np.arange(bits, max(int(bits) - 8 * 128, 0), -1, dtype=np.uint32) << 16).view(np.float32)
+    s = K.round_bf16(np.float64(top) / 6)
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * s
+    x = np.concatenate([x, mids.astype(np.float32)])
+    if dtype == "f32":
+        x = np.concatenate([x, np.nextafter(x, np.float32(0)), np.nextafter(x, np.float32(np.inf))])
+        x = x[x <= top]
+    x = synth.round_to(x, dtype)
+    n = -(-len(x) // 31)
+    body = np.zeros(31 * n, np.float32)
+    body[:len(x)] = x
+    rows = np.concatenate([np.full((n, 1), top, np.float32), body.reshape(n, 31) * np.where(np.arange(31) % 3 == 0, -1, 1)], 1)
+    rows = np.tile(rows.astype(np.float32), (1, 2))           # two groups of a head
+    cache = tg.KV4Cache.zeros(-(-n // 16), 16, 1, 64)
+    d = _dev(rows, synth.torch_dtype(dtype))
+    slots = torch.arange(n, dtype=I32, device=DEV)
+    tg.tg_kv4_store(cache, d, d, None, slots)
+    k, v = torch.empty(n, 64, device=DEV), torch.empty(n, 64, device=DEV)
+    tg.tg_kv4_load(cache, slots, k, v)
+    want = K.kv4_quantize(rows)[0]
+    np.testing.assert_array_equal(k.cpu().numpy(), want)
+    np.testing.assert_array_equal(v.cpu().numpy(), want)
+
+
 def test_store_non_finite_groups_read_back_as_nan_and_leave_their_neighbours():
     x = torch.randn(4, 128, device=DEV)
     x[0, 3], x[1, 40], x[2, 100] = math.inf, -math.inf, math.nan
