@@ -721,6 +721,78 @@ def decode_extras(args, run=None):
     return dec
 
 
+def run_paged(args):
+    """Decode over the paged 4-bit cache, one JSON line per workload: the
+    attention call (L2 flushed before it, the flush timed apart and taken off)
+    for one request at the cache lengths of --decode and for a ragged batch of
+    33 requests of up to 8321 rows, and the whole decode step of that batch
+    (page tables, q/k norm and rotation, rows into the cache, attention) as one
+    CUDA graph.  Bytes are the codes, scales and biases of every row; 16/8 heads
+    x 128, bf16."""
+    import torch
+    from learned_token_pruning_b200 import pipeline, tokengate as tg
+    dev = torch.device("cuda", torch.cuda.current_device())
+    peaks = load_peaks()
+    hq, hkv, dh, page = 16, 8, 128, 64
+    flush = torch.empty(L2_FLUSH_BYTES, dtype=torch.uint8, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    reps = max(args.steps, 10)
+
+    def graph_of(body):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            body()
+        return gr
+
+    def replay_ms(gr):
+        gr.replay()
+        torch.cuda.synchronize(dev)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record(stream)
+        for _ in range(reps):
+            gr.replay()
+        b.record(stream)
+        torch.cuda.synchronize(dev)
+        return a.elapsed_time(b) / reps
+
+    def flushed(call):
+        def body():
+            flush.zero_()
+            call()
+        return body
+
+    ragged = [8321 - (i * 251) % 8192 for i in range(33)]
+    for name, lens in (("qwen3_1.7b_decode_kv4_n16384_k2000", [2129]), ("qwen3_1.7b_decode_kv4_n131072_k8192", [8321]),
+                       ("qwen3_1.7b_decode_kv4_unpruned_n131072", [131137]), ("qwen3_1.7b_decode_kv4_batch33", ragged)):
+        n, rows = len(lens), sum(lens)
+        steps = max(args.warmup, 3) + 2 * (reps + 4)   # rows the timed steps may add
+        g = torch.Generator(device=dev).manual_seed(rows)
+        b = pipeline.PagedDecodeBatch(n, max(lens) + steps, sum(-(-(x + steps) // page) for x in lens), page, hq=hq, hkv=hkv,
+                                      head_dim=dh, device=dev, head_gain=torch.rand(hq, device=dev, generator=g) + 0.5,
+                                      head_temp=torch.rand(hq, device=dev, generator=g) * 0.4 + 0.8)
+        kv = torch.randn(2, rows, hkv * dh, device=dev, generator=g).to(torch.bfloat16)
+        b.admit(torch.tensor(lens, dtype=torch.int32, device=dev), kv[0], kv[1], torch.randn(rows, device=dev, generator=g))
+        b.qkv.normal_(generator=g)
+        b.ratio.fill_(0.9)
+        attend = lambda: tg.tg_kv4_decode_attention(b.cache, b.q, b.tables, b.lens, b.head_gain, b.head_temp, b.ratio,
+                                                    b.sm_scale, b.out, b.ws, b.lse, flags=tg.TG_WS_KEPT_ZERO)
+        for _ in range(max(args.warmup, 3)):
+            flush.zero_()
+            attend()
+        base = replay_ms(graph_of(lambda: flush.zero_()))
+        ms = replay_ms(graph_of(flushed(attend))) - base
+        for _ in range(max(args.warmup, 3)):
+            b.step()
+        step_ms = replay_ms(graph_of(flushed(b.step))) - base
+        tg.tg_check_device_error()
+        nbytes = rows * (2 * hkv * (dh // 2 + dh // 16) + 4)
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        print(json.dumps({"mode": "paged", "workload": name, "requests": n, "cache_rows": rows, "page_rows": page,
+                          "us": ms * 1e3, "cache_bytes": nbytes, "gbs": gbs, "frac_hbm": gbs / peaks["hbm_gbs"],
+                          "step_us": step_ms * 1e3, "peak_source": peaks["source"],
+                          "l2": "flushed before every call"}), flush=True)
+
+
 def run_backward(args):
     """Backward of token-gated attention at the kept rows of the 16K- and
     128K-token prompts (Qwen3-1.7B heads, bf16), per call, L2 flushed before
@@ -1085,6 +1157,7 @@ def main(argv=None):
     ap.add_argument("--sweep", action="store_true", help="budget-sweep and 128K single-layer workloads")
     ap.add_argument("--stack", action="store_true", help="28-layer stack TTFT, pruned vs unpruned")
     ap.add_argument("--decode", action="store_true", help="decode attention over the gated KV cache, per call")
+    ap.add_argument("--paged", action="store_true", help="decode over the paged 4-bit cache: the attention call and the step")
     ap.add_argument("--batch", action="store_true", help="varlen batch of eight requests vs one at a time")
     ap.add_argument("--ncu-decode", action="store_true", help="one decode call on a 131137-row cache (profiling)")
     ap.add_argument("--backward", action="store_true", help="backward of gated attention at the kept-row counts")
@@ -1109,6 +1182,9 @@ def main(argv=None):
         return
     if args.stack:
         run_stack(args)
+        return
+    if args.paged:
+        run_paged(args)
         return
     if args.decode:
         run_decode(args)

@@ -318,6 +318,90 @@ class PrunedPrefillStack:
         return self.h
 
 
+class PagedDecodeBatch:
+    """Decode of a batch of pruned prompts over one paged 4-bit cache of gated
+    keys and values (one layer's).  Pages, slots and lengths live on the device:
+
+      admit()  the kept rows of new prompts enter the cache (and finished
+               requests give their pages back): page tables, then the rows;
+      step()   one new token for every request: page tables, q/k norm and
+               rotation, the new rows into the cache, attention over it.
+
+    A step is five library kernels on one stream and can be captured: the same
+    graph then serves every following step."""
+
+    def __init__(self, nreq: int, max_rows: int, num_pages: int, page_rows: int, *, hq: int, hkv: int, head_dim: int,
+                 head_gain, head_temp, w_q_norm=None, w_k_norm=None, qk_norm: bool = True, rope_theta: float = 1.0e6,
+                 norm_eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+        dev, i32 = torch.device(device), torch.int32
+        self.hq, self.hkv, self.head_dim, self.page_rows = hq, hkv, head_dim, page_rows
+        self.norm = (w_q_norm, w_k_norm, norm_eps, rope_theta, qk_norm)
+        self.head_gain, self.head_temp, self.sm_scale = head_gain, head_temp, head_dim ** -0.5
+        self.cache = tg.KV4Cache.zeros(num_pages, page_rows, hkv, head_dim, device=dev)
+        self.lens = torch.zeros(nreq, dtype=i32, device=dev)
+        self.tables = torch.full((nreq, -(-max_rows // page_rows)), -1, dtype=i32, device=dev)
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=i32, device=dev)   # page 0 is taken first
+        self.n_free = torch.full((1,), num_pages, dtype=i32, device=dev)
+        self.row_start = torch.zeros(nreq + 1, dtype=i32, device=dev)
+        self.one = torch.ones(nreq, dtype=i32, device=dev)
+        self.slots = torch.empty(nreq, dtype=i32, device=dev)
+        # one step's inputs and result: [q | k | v] of the projection, positions, temperature ratios
+        self.qkv = torch.zeros(nreq, (hq + 2 * hkv) * head_dim, dtype=dtype, device=dev)
+        self.pos = torch.zeros(nreq, dtype=i32, device=dev)
+        self.ratio = torch.ones(nreq, dtype=torch.float32, device=dev)
+        self.out = torch.empty(nreq, hq * head_dim, dtype=dtype, device=dev)
+        self.lse = torch.empty(nreq, hq, dtype=torch.float32, device=dev)
+        self.q = self.qkv[:, :hq * head_dim]
+        self.k = self.qkv[:, hq * head_dim:(hq + hkv) * head_dim]
+        self.v = self.qkv[:, (hq + hkv) * head_dim:]
+        self.ws = torch.zeros(tg.kv4_decode_workspace_bytes(hq, hkv, head_dim), dtype=torch.uint8, device=dev)
+        self._graph = None
+
+    def _pages(self, new_rows, release, slots, stream):
+        tg.tg_page_tables(self.lens, new_rows, release, self.page_rows, self.tables, self.free_pages, self.n_free, self.lens,
+                          self.n_free, slots, self.row_start, stream)
+
+    def admit(self, new_rows, k, v, bias, release=None, stream=None):
+        """new_rows int32 [nreq] on the device: rows each request gets; k / v [rows, hkv*head_dim] their keys (rotated)
+        and values by request, bias fp32 [rows] their importance; release uint8 [nreq] (or None): requests that give
+        up what they hold first."""
+        slots = torch.empty(k.shape[0], dtype=torch.int32, device=k.device)
+        self._pages(new_rows, release, slots, stream)
+        tg.tg_kv4_store(self.cache, k, v, bias, slots, stream)
+
+    def step(self, stream=None):
+        """One token for every request from self.qkv, self.pos and self.ratio; the result is left in self.out.  q and k
+        are normalised and rotated in place."""
+        wq, wk, eps, theta, norm = self.norm
+        self._pages(self.one, None, self.slots, stream)
+        tg.tg_qk_norm_rope(self.q, self.k, self.head_dim, self.pos, wq, wk, eps, theta, self.q, self.k, qk_norm=norm,
+                           stream=stream)
+        tg.tg_kv4_store(self.cache, self.k, self.v, None, self.slots, stream)
+        tg.tg_kv4_decode_attention(self.cache, self.q, self.tables, self.lens, self.head_gain, self.head_temp, self.ratio,
+                                   self.sm_scale, self.out, self.ws, self.lse, flags=tg.TG_WS_KEPT_ZERO, stream=stream)
+        return self.out
+
+    def capture(self):
+        """Record step() without taking one: lengths, tables and the free list are put back afterwards, so the first
+        replay is the next step.  (The eager call before the recording sets the kernels' attributes up.)"""
+        state = [t.clone() for t in (self.lens, self.tables, self.free_pages, self.n_free, self.qkv)]
+        self.step()
+        for t, old in zip((self.lens, self.tables, self.free_pages, self.n_free, self.qkv), state):
+            t.copy_(old)
+        torch.cuda.synchronize(self.out.device)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            self.step()
+        self._graph = graph
+        return graph
+
+    def replay(self):
+        if self._graph is None:
+            self.capture()
+        self._graph.replay()
+        return self.out
+
+
 def stack_weights_from_synth(w: synth.Workload, n_layers: int, device="cuda"):
     """Layer and head parameters of synth.py (the oracle reads the same arrays)."""
     dt = synth.torch_dtype(w.dtype)
