@@ -481,8 +481,9 @@ int tg_linear(const void* x, int64_t ldx, const void* w, void* y, int64_t ldy, i
  * that cannot be met (too few pages, a table or slots too short, a negative or
  * too large length) sets the device error word (TG_ERR_DEVICE_CHECK), and then
  * nothing changes but slots (all -1) and row_start (all 0).
- * nreq <= 4096; nreq == 0 only marks the slots.  Errors: TG_ERR_INVALID_ARG (null pointer, sizes < 0,
- * page_rows or max_pages < 1), TG_ERR_UNSUPPORTED (nreq > 4096).
+ * Any page_rows >= 1; nreq <= 4096, max_pages * page_rows and nslots <= 2^30; nreq == 0
+ * only marks the slots.  Errors: TG_ERR_INVALID_ARG (null pointer, sizes < 0, page_rows
+ * or max_pages < 1), TG_ERR_UNSUPPORTED (past those limits).
  */
 int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
                    int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
@@ -596,7 +597,7 @@ int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, v
  * g = h / (hq / hkv), and its rows c < lens[r]:
  *     l_c = head_temp[h] * ratio[r] * sm_scale * (q_h . k_c) + head_gain[h] * bias[c]
  *     out_h = sum_c softmax_c(l) v_c,   lse_h = log sum_c exp(l_c)
- * A key whose bias is -infinity is left out, whatever its row holds (head_gain > 0).
+ * A key whose bias is -infinity is left out, whatever its row holds and whatever the gain.
  * A request with no row left gets zeros and lse -infinity.
  *   q      device, dtype, request r's head h at q + r*ldq + h*head_dim
  *   tables device int32 [nreq][max_pages], lens device int32 [nreq] (as
@@ -605,11 +606,13 @@ int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, v
  *   out    device, dtype, rows as q;  lse device fp32 [nreq][hq] or NULL
  *   ws     device workspace of tg_workspace_bytes(TG_OP_KV4_DECODE, 0, 0, 0, 0, shape)
  *          bytes (shape gives hq, hkv, head_dim), 16-byte aligned; the size depends on
- *          the SM count, not on the batch
- *   flags  0, or TG_WS_KEPT_ZERO: ws is zero-filled or as the previous successful
- *          call with this flag left it, and the call launches no memset
+ *          the SM count, not on the batch.  Its contents on entry do not matter; calls
+ *          that may overlap on the GPU need one each
+ *   flags  0 or TG_WS_KEPT_ZERO (the same here: the call keeps nothing in ws)
  * bf16 or fp32 queries; head_dim in {64, 128}; at most 8 query heads per KV head; nreq
- * <= 4096; nreq == 0 does nothing.  A length that is negative or beyond the table
+ * <= 4096, max_pages * page_rows <= 2^30, hkv * nreq * (max_pages * page_rows / 32 + 3)
+ * < 2^31; nreq == 0 does nothing.  bf16 queries: weights rounded to 11 bits, fp32 sums; fp32 queries:
+ * queries and weights to 22 bits, fp32 sums.  A length that is negative or beyond the table
  * counts as 0, a page id outside the cache as page 0, and either sets the device error word.
  * The lengths are read on the device, so a captured call follows them.
  * Errors: TG_ERR_INVALID_ARG, TG_ERR_UNSUPPORTED, TG_ERR_SHAPE, TG_ERR_ALIGN (q and

@@ -1910,8 +1910,8 @@ int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* 
     return fail(TG_ERR_INVALID_ARG, "null pointer");
   if (nreq > 0 && (!lens || !new_rows || !tables || !lens_out)) return fail(TG_ERR_INVALID_ARG, "null pointer");
   if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
-  if (int64_t(max_pages) * page_rows >= (int64_t(1) << 31))
-    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
+  if (int64_t(max_pages) * page_rows > (int64_t(1) << 30) || nslots > (1 << 30))
+    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows and nslots must be <= 2^30");
   tg::PageTableParams p{};
   p.lens = lens;
   p.new_rows = new_rows;
@@ -2082,8 +2082,8 @@ int tg_kv4_decode_attention(const tg_kv4_cache* cache, const void* q, int64_t ld
   const int group = hq / cache->hkv;
   if (group > tg::kKv4MaxGroup) return fail(TG_ERR_UNSUPPORTED, "at most %d query heads per KV head", tg::kKv4MaxGroup);
   if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
-  if (int64_t(max_pages) * cache->page_rows >= (int64_t(1) << 31))
-    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be < 2^31");
+  if (int64_t(max_pages) * cache->page_rows > (int64_t(1) << 30))
+    return fail(TG_ERR_UNSUPPORTED, "max_pages * page_rows must be <= 2^30");
   // the cost of the work is counted in 32 bits
   if ((2 * (int64_t(max_pages) * cache->page_rows / tg::kKv4Tile + 1) + 1) * nreq >= (int64_t(1) << 31) / cache->hkv)
     return fail(TG_ERR_UNSUPPORTED, "nreq * max_pages * page_rows * hkv is too large");

@@ -166,7 +166,8 @@ def test_page_tables_validation(L):
     assert call(free=None) == 1
     assert call(nreq=-1) == 1 and call(page=0) == 1 and call(mp=0) == 1 and call(cap=-1) == 1 and call(ns=-1) == 1
     assert call(nreq=4097) == 4
-    assert call(page=1 << 20, mp=1 << 11) == 4
+    assert call(page=1 << 20, mp=1 << 11) == 4 and call(page=1 << 15, mp=(1 << 15) + 1) == 4
+    assert call(ns=(1 << 30) + 1) == 4
 
 
 def test_qk_rope_validation(L):
@@ -231,7 +232,8 @@ def test_kv4_decode_validation(L):
     assert call(flags=2) == 1 and call(dt=3) == 1 and call(nreq=-1) == 1 and call(mp=0) == 1
     assert call(hq=12) == 1                                   # not a multiple of the KV heads
     assert call(hq=72, ldq=9216, ldo=9216) == 4               # nine query heads per KV head
-    assert call(nreq=4097) == 4 and call(mp=1 << 28) == 4
+    assert call(nreq=4097) == 4 and call(mp=1 << 28) == 4 and call(mp=(1 << 26) + 1) == 4
+    assert call(nreq=4096, mp=1 << 20) == 4                   # more work than 32 bits count
     assert call(c=_cache(page_rows=20)) == 1 and call(c=_cache(head_dim=32)) == 4
     assert call(ldq=2040) == 2 and call(ldo=100) == 2
     assert call(q=OFF) == 3 and call(ws=OFF) == 3 and call(ldo=2052) == 3
