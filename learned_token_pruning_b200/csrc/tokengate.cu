@@ -1770,16 +1770,35 @@ int check_qk(int dtype, int64_t m, int32_t hq, int32_t hkv, int32_t head_dim, fl
   return TG_OK;
 }
 
-// Warps that share a row: one per pass while that is about a wave of the GPU (16 warps an SM),
-// where a row's passes one after the other are what takes time, else one.
-int qk_rope_split(int64_t m, int passes) { return m * passes <= 32 * int64_t(sm_count()) ? passes : 1; }
+// blocks of either kernel at most: two an SM (the backward's workspace holds a partial of each)
+int qk_rope_blocks() { return 2 * sm_count(); }
+
+// Rows are dealt to the warps whole or in parts of equal numbers of passes, whichever ends
+// first: rounds of items times a part's passes and its table of angles, which takes as
+// long as about a pass and a half.  Whole rows in rounds of 16 warps an SM leave the last round
+// idle, parts repeat the angles: 16 + 8 heads of 128, bf16, whole against cut, backward of
+// 592 rows 12.1 / 10.3 us, 3000 rows 22.6 / 22.0; parts chosen with half that price for the
+// table (forward of 8256 rows in two parts) 20.3 us against 18.6 whole.
+void qk_rope_cut(tg::QkRopeParams& p, int passes, int most) {
+  p.split = 1;
+  p.per = passes;
+  const int64_t warps = int64_t(most) * tg::kRopeWarps;
+  if (p.m > 8 * warps) return;  // the last round hardly counts
+  int64_t best = INT64_MAX;
+  for (int n = 1; n <= std::min(passes, 32); ++n) {
+    const int per = (passes + n - 1) / n, parts = (passes + per - 1) / per;
+    const int64_t cost = (p.m * parts + warps - 1) / warps * (2 * per + 3);
+    if (cost < best) {
+      best = cost;
+      p.split = parts;
+      p.per = per;
+    }
+  }
+}
 
 int qk_rope_passes(int hq, int hkv, int head_dim) {
   return head_dim == 128 ? tg::RopePasses<128>(hq, hkv).all : tg::RopePasses<64>(hq, hkv).all;
 }
-
-// blocks of either kernel at most: two an SM (the backward's workspace holds a partial of each)
-int qk_rope_blocks() { return 2 * sm_count(); }
 
 }  // namespace
 
@@ -1821,7 +1840,7 @@ int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int 
   p.k_out = k_out;
   p.ldqo = ldqo;
   p.ldko = ldko;
-  p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
+  qk_rope_cut(p, qk_rope_passes(hq, hkv, head_dim), qk_rope_blocks());
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_blocks())));
   const dim3 block(32 * tg::kRopeWarps);
   const tg::RopeTable& tab = rope_table(rope_theta, head_dim);
@@ -1882,7 +1901,7 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
   p.dq = dq;
   p.dk = dk;
   p.part = sums ? static_cast<float*>(ws) : nullptr;
-  p.split = qk_rope_split(m, qk_rope_passes(hq, hkv, head_dim));
+  qk_rope_cut(p, qk_rope_passes(hq, hkv, head_dim), qk_rope_blocks());
   const int blocks = static_cast<int>(
       std::min<int64_t>((m * p.split + tg::kRopeWarps - 1) / tg::kRopeWarps, qk_rope_blocks()));
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * tg::kRopeWarps);
