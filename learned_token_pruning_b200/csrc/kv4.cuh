@@ -48,11 +48,12 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Cache& c, int32_t slot, int 
 // takes its share of the page moves and of the slots.  The cluster barriers
 // order the reads of the old state before the writes of the new one, so the
 // state may be updated in place.  Bound by latency: the two barriers and the
-// dependent loads (length -> page -> slot).
+// dependent loads (length -> page -> slot).  Device time: one more row for 56 of 64
+// requests 6.6 us, 129828 rows for 1000 requests (pages of 16, 0.6 MB) 12.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 constexpr int kTabMaxReq = 4096;
-constexpr int kTabChunk = 256;
+constexpr int kTabTimes = 8;
 constexpr int kTabPer = kTabMaxReq / kTabThreads;  // requests per thread at most
 
 struct PageTableParams {
@@ -205,20 +206,23 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
     const int first = (s_len[r] + p.page_rows - 1) / p.page_rows;
     p.tables[static_cast<int64_t>(r) * p.max_pages + first + (i - s_take[r])] = __ldcg(p.free_pages + (top - 1 - i));
   }
-  // 256 neighbouring slots to a warp: one search for the first row's request, then short
-  // walks, and the eight page ids a lane needs on their way together (129828 slots of
-  // 1000 requests: 33 us with a search for every slot)
+  // A warp takes 32 neighbouring slots up to eight times in a row, as often as it takes to go
+  // round once: one search for the first row's request, then short walks, and the page ids a
+  // lane needs on their way together.  129828 slots of 1000 requests, 16 CTAs: eight times
+  // 12.0 us, twice 15.5; one slot for each of 1000 requests, where a walk passes as many
+  // requests as slots: 15.1 and 9.0.
   const int lane = threadIdx.x & 31;
-  for (int c = t0 >> 5; c * kTabChunk < p.nslots; c += step >> 5) {
-    const int i0 = c * kTabChunk + lane;
+  const int times = max(1, min(kTabTimes, (p.nslots + step - 1) / step));
+  for (int c = t0 >> 5; static_cast<int64_t>(c) * times * 32 < p.nslots; c += step >> 5) {
+    const int i0 = c * times * 32 + lane;
     int r = i0 < nrows ? find_request(s_rows, p.nreq, i0) : 0;
-    int32_t id[kTabChunk / 32], off[kTabChunk / 32];
+    int32_t id[kTabTimes], off[kTabTimes];
 #pragma unroll
-    for (int k = 0; k < kTabChunk / 32; ++k) {
+    for (int k = 0; k < kTabTimes; ++k) {
       const int i = i0 + 32 * k;
       id[k] = -1;
       off[k] = -1;
-      if (i < nrows) {
+      if (k < times && i < nrows) {
         while (s_rows[r + 1] <= i) ++r;
         const int32_t at = s_len[r] + (i - s_rows[r]);
         const int32_t page = at / p.page_rows, held = (s_len[r] + p.page_rows - 1) / p.page_rows;
@@ -229,10 +233,10 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
       }
     }
 #pragma unroll
-    for (int k = 0; k < kTabChunk / 32; ++k) {
+    for (int k = 0; k < kTabTimes; ++k) {
       const int i = i0 + 32 * k;
       if (id[k] < 0 && off[k] >= 0) raise_error(kErrPageTable, 4);
-      if (i < p.nslots) p.slots[i] = id[k] < 0 ? -1 : id[k] * p.page_rows + off[k];
+      if (k < times && i < p.nslots) p.slots[i] = id[k] < 0 ? -1 : id[k] * p.page_rows + off[k];
     }
   }
   for (int i = t0; i <= p.nreq; i += step) {
