@@ -528,7 +528,7 @@ int tg_qk_norm_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, int 
  *   ws         device workspace of tg_workspace_bytes(TG_OP_QK_ROPE_BWD, 0, m, 0, 0,
  *              shape) bytes (shape gives head_dim), 16-byte aligned; may be NULL
  *              when dw_q and dw_k are NULL or qk_norm == 0.  Its contents on
- *              entry do not matter.
+ *              entry do not matter; calls that may overlap on the GPU need one each.
  * fp32 sums in a fixed order, no atomics: reruns are bit-identical.  m == 0
  * only zeroes dw_q and dw_k.  Errors: the forward's, TG_ERR_WORKSPACE.
  */
@@ -573,8 +573,8 @@ typedef struct {
  *   bias   device fp32 [rows] or NULL (0); ignored when the cache has none
  *   slots  device int32 [rows]: where each row goes (tg_page_tables' slots); a
  *          negative slot leaves its row out.  A slot past the cache sets the device error
- *          word and is left out.  With a slot given twice it is unspecified which
- *          row's groups stay.
+ *          word and is left out.  With a slot given twice, what it holds is
+ *          unspecified (a mixture of the rows).
  * rows == 0 does nothing.  Errors: TG_ERR_INVALID_ARG (null pointer, rows < 0,
  * page_rows, hkv, num_pages, dtype), TG_ERR_UNSUPPORTED (head_dim, 2^31 slots or rows),
  * TG_ERR_SHAPE (leading dimension), TG_ERR_ALIGN.

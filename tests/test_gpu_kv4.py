@@ -80,6 +80,12 @@ def test_page_tables(nreq, page, top_len, new, done, in_place):
     _tables_same(t, want)
 
 
+@pytest.mark.parametrize("nreq,page,top_len,new,done", [(300, 16, 10, 150, 20), (1000, 16, 0, 261, 0), (1000, 64, 8321, 1, 30),
+                                                        (60, 32, 5, 900, 7)])
+def test_page_tables_slots_in_runs_of_several_lengths(nreq, page, top_len, new, done):
+    test_page_tables(nreq, page, top_len, new, done, False)
+
+
 def test_page_tables_without_a_release_vector_and_without_requests():
     case = _tables_case(9, 16, 1, 60, 4)
     t = _tables_call(case, 16, release=False)

@@ -156,6 +156,14 @@ def test_backward_prompt_rows_and_reruns_are_identical():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("m,hq,hkv,d,dtype", [(593, 16, 8, 128, "bf16"), (1187, 10, 2, 128, "bf16"), (2999, 6, 2, 64, "f32"),
+                                              (700, 70, 7, 64, "bf16"), (310, 40, 33, 128, "f32")])
+def test_rows_cut_into_parts(m, hq, hkv, d, dtype):
+    # a row's passes shared by several warps, the last part shorter, q and k in one part
+    _check_forward(m, hq, hkv, d, dtype, seed=m)
+    _check_backward(m, hq, hkv, d, dtype, seed=m + 1)
+
+
 def test_backward_against_differences_of_the_forward():
     # central differences of the CUDA forward in fp32, along random directions
     m, hq, hkv, d, h = 5, 2, 1, 64, 2.0 ** -6
