@@ -22,7 +22,8 @@
 //   Both factors meet a power of two that keeps them in fp16's range: the query one
 //   per head (its largest value lands at 2^8), the weights one per head and scale
 //   group (weight 1 times the largest value scale met so far lands at 2^6 .. 2^7; the
-//   running exponent moves with the softmax's reference).
+//   running exponent moves with the softmax's reference, and follows the products where a huge
+//   row has next to no weight).
 //   The 8 columns hold HP heads (2, 4 or 8) times 8 / HP scale groups: with two
 //   heads, one B operand serves all four groups of D = 128.  A lane reads the
 //   accumulator columns of its own group and leaves the others.
@@ -37,17 +38,19 @@
 // reruns are bit-identical.
 //
 // Measured (16 + 8 heads of 128, bf16 queries, both kernels): 131137 rows of one request, pages
-// of 128: 40 us, 152 MB, 3.8 TB/s (58 % of a copy's 6.55); pages of 16: 45; a ragged batch of 33
-// requests of up to 8321 rows, pages of 16: 47.5; 2129 rows: 10.  About 25 us of the 40
+// of 128: 40.6 us, 152 MB, 3.7 TB/s (57 % of a copy's 6.55); pages of 16: 45.7; a ragged batch of
+// 33 requests of up to 8321 rows, pages of 16: 48.3; 2129 rows: 10.4.  About 25 us of the 40
 // are the stream itself, the same when the cache sits in L2: 17.7 M warp instructions at 0.46 a
 // cycle and scheduler, with the logic pipe that takes the codes apart 43 % busy and the matrix
-// pipe 21 %.  The other 15 are latency: the plan, the first page ids and keys, a run's
+// pipe 21 %.  Finite logits and units for any finite bias and value scale cost 0.5 us of them.  The other 15 are latency: the plan, the first page ids and keys, a run's
 // whole tiles, the pieces and the second kernel.
 // Tried: tiles of 32 keys, 41 .. 52 us; 16-byte copies by every lane in place of the bulk
 // copies, 51.5 (pages of 16: 55.7 against 56.5 then), for the scales and biases alone 41.7 (pages
 // of 16: 43.6 against 45.2); two or three CTAs per SM, 42 .. 59; merging by a ticket
 // in this kernel, 45.2.
 #pragma once
+
+#include <cfloat>
 
 #include "attn_tc.cuh"
 #include "common.cuh"
@@ -413,6 +416,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
 
   uint32_t qf[kSplit ? 2 : 1][NG][2][2];
   float o[NG][2][4];
+  float bias_most = 0.0f;  // gain times a bias up to this is finite in base 2
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, a0 = 0.0f, a1 = 0.0f, g0 = 0.0f, g1 = 0.0f;
   int ex[NB];
 
@@ -452,6 +456,10 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
     a1 = hd + 1 < group ? p.temp[h0 + hd + 1] * rs * b1 : 0.0f;
     g0 = hd < group ? p.gain[h0 + hd] * 1.4426950408889634f : 0.0f;
     g1 = hd + 1 < group ? p.gain[h0 + hd + 1] * 1.4426950408889634f : 0.0f;
+    float gmax = fmaxf(fabsf(g0), fabsf(g1));
+    gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, 1));
+    gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, 2));
+    bias_most = FLT_MAX / fmaxf(gmax, 1.0f) * 0.999f;
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.0f;
 #pragma unroll
@@ -526,15 +534,22 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       // Keys past the request's rows and keys with bias -infinity: their scales and biases
       // are zeroed (whatever they hold must not meet the sums) and their logits set to -infinity.
       uint32_t dead[(MT + 1) / 2];
-      bool any_dead = false;
+      bool any_dead = false, huge = false;
 #pragma unroll
       for (int h = 0; h < (MT + 1) / 2; ++h) {
         const int key = 32 * h + lane;
         bool d = false;
-        if (key < kKv4Tile) d = key >= rows || *reinterpret_cast<const float*>(smem + at0 + stage + Ring::kBias + 4 * key) == -INFINITY;
+        if (key < kKv4Tile && key < rows) {
+          const float bias = *reinterpret_cast<const float*>(smem + at0 + stage + Ring::kBias + 4 * key);
+          d = bias == -INFINITY;
+          huge |= fabsf(bias) > bias_most;  // infinities too
+        } else {
+          d = true;
+        }
         dead[h] = __ballot_sync(0xffffffffu, d);
         any_dead |= dead[h] != 0;
       }
+      huge = __any_sync(0xffffffffu, huge);
       if (any_dead) {
 #pragma unroll
         for (int h = 0; h < (MT + 1) / 2; ++h)
@@ -591,6 +606,14 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
         x[mt][2] = fmaf(a0, x[mt][2], g0 * bias1);
         x[mt][3] = fmaf(a1, x[mt][3], g1 * bias1);
       }
+      if (huge) {  // a finite bias makes a finite logit
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (fabsf(x[mt][c]) == INFINITY && fabsf(*reinterpret_cast<const float*>(smem + bbase + stage + 64 * mt + 32 * (c >> 1))) < INFINITY)
+              x[mt][c] = copysignf(FLT_MAX, x[mt][c]);
+      }
       if (any_dead) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -640,17 +663,62 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
 #pragma unroll
       for (int b = 0; b < NB; ++b) moved |= static_cast<int>(vtop[b] >> 23) > ex[b];
       if (__any_sync(0xffffffffu, moved)) {
-        const float n0 = fmaxf(m0, rows_max(t0)), n1 = fmaxf(m1, rows_max(t1));
+        const float tile0 = rows_max(t0), tile1 = rows_max(t1), n0 = fmaxf(m0, tile0), n1 = fmaxf(m1, tile1);
         const float d0 = n0 == m0 ? 0.0f : m0 - n0, d1 = n1 == m1 ? 0.0f : m1 - n1;
         l0 *= kv4_ex2(d0);
         l1 *= kv4_ex2(d1);
+        // The unit follows the largest value scale, unless that one's weight makes it more than 2^12
+        // too large for what is summed (a huge row behind a finite mask): then the largest product
+        // of a weight and a scale, or what the sums so far come to under the new reference.  The
+        // products are looked at only where scales are that far apart, or all of the tile's
+        // weights small.
+        const bool real0 = hd < group, real1 = hd + 1 < group, near = (real0 && tile0 == n0) || (real1 && tile1 == n1);
+        const float gone = fmaxf(fmaxf(real0 ? d0 : -300.0f, real1 ? d1 : -300.0f), -300.0f);
+        int need[NB], most[NB];
+        bool apart = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          uint32_t v = vtop[b];
+          need[b] = max(ex[b] + (gone > -12.0f ? 0 : static_cast<int>(ceilf(gone))), kKv4WeightExp + 1);
+          int v = min(static_cast<int>(vtop[b] >> 23), 254);  // NaN scales (255) set no unit
           v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = max(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const int nex = max(ex[b], min(static_cast<int>(v >> 23), 254));  // NaN scales (255) set no unit
+          most[b] = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          uint32_t least = 0xffffffffu;  // of this lane's scales that are not 0
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) least = min(least, min(vs0[mt][b] - 1, vs1[mt][b] - 1));
+          apart |= real0 && most[b] - need[b] > 12 && (!near || most[b] - static_cast<int>(least >> 23) > 12);
+        }
+        apart = __any_sync(0xffffffffu, apart);
+        if (apart) {
+          const float r0 = real0 ? fmaxf(n0, -FLT_MAX) : INFINITY, r1 = real1 ? fmaxf(n1, -FLT_MAX) : INFINITY;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            int u = need[b];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const float f0 = fmaxf(fmaxf(x[mt][0] - r0, x[mt][1] - r1), -300.0f);
+              const float f1 = fmaxf(fmaxf(x[mt][2] - r0, x[mt][3] - r1), -300.0f);
+              u = max(u, max(min(static_cast<int>(vs0[mt][b] >> 23), 254) + static_cast<int>(ceilf(f0)),
+                             min(static_cast<int>(vs1[mt][b] >> 23), 254) + static_cast<int>(ceilf(f1))));
+            }
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, s));
+            // scale times factor stays finite: above this a weight is 2^-103 at most
+            const uint32_t cap = u < 254 - 110 ? static_cast<uint32_t>(u + 110) << 23 : 0x7f800000u;
+            need[b] = u;
+            if (real0 && most[b] - u > 12) {
+              most[b] = u;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                if (vs0[mt][b] < 0x7f800000u) vs0[mt][b] = min(vs0[mt][b], cap);
+                if (vs1[mt][b] < 0x7f800000u) vs1[mt][b] = min(vs1[mt][b], cap);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int nex = max(need[b], most[b]);
           const float de = static_cast<float>(ex[b] - nex);
           const float c0 = kv4_ex2(d0 + de), c1 = kv4_ex2(d1 + de);
           ex[b] = nex;

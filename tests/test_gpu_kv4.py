@@ -457,6 +457,75 @@ def test_attention_every_key_at_the_lowest_finite_bias():
     assert (np.abs(out[0].float().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (6, 2, 64), (8, 1, 128)])
+def test_attention_every_key_at_the_types_lowest_value(hq, hkv, d, dtype):
+    # gain * bias passes the largest float in base 2 (and for gains above 1 in any base): the logits
+    # are equal all the same, and the output is the mean of the values
+    b = Batch([130, 9], hq, hkv, d, 16, dtype, seed=40)
+    b.bias[:] = np.finfo(np.float32).min
+    b.gain[:] = np.linspace(0.5, 2.0, hq)
+    b.store()
+    out, lse = b.run()
+    half, slack = (2.0 ** -8, 2.0 ** -10) if dtype == "bf16" else (2.0 ** -24, 1e-4)
+    for r, rows in ((0, slice(0, 130)), (1, slice(130, 139))):
+        v = np.repeat(K.kv4_quantize(b.v[rows])[0], hq // hkv, 1)
+        err = np.abs(out[r].float().cpu().numpy().reshape(hq, d) - v.mean(0))
+        assert (err <= half * np.abs(v.mean(0)) + slack * np.abs(v).mean(0)).all()
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_lowest_value_under_a_negative_gain_takes_all_the_weight(dtype):
+    b = Batch([100], 4, 2, 64, 16, dtype, seed=41)
+    b.gain[:] = [-1.0, 1.0, -2.0, 0.5]
+    b.bias[:] = 0.0
+    b.bias[30:40] = np.finfo(np.float32).min
+    b.store()
+    out, _ = b.run()
+    v = np.repeat(K.kv4_quantize(b.v)[0][30:40], 2, 1)
+    got = out[0].float().cpu().numpy().reshape(4, 64)
+    for h in (0, 2):
+        assert (np.abs(got[h] - v[:, h].mean(0)) <= 2.0 ** -8 * np.abs(v[:, h].mean(0)) + 2.0 ** -10 * np.abs(v[:, h]).mean(0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (6, 2, 64), (8, 1, 128), (3, 1, 128)])
+@pytest.mark.parametrize("low", [-3.4e38, -300.0])
+def test_attention_huge_values_behind_a_finite_mask_leave_the_others_exact(low, hq, hkv, d, dtype):
+    # rows without weight must not set the unit that the others' weights are rounded in
+    b = Batch([200, 31], hq, hkv, d, 16, dtype, seed=42)
+    b.gain[:] = 1.0
+    off = np.random.default_rng(2).permutation(231)[:40]
+    b.bias[off] = low
+    b.v[off] = synth.round_to(b.v[off] * np.float32(2.0 ** 90 if low < -1e38 else 2.0 ** 60), "bf16")
+    b.store()
+    b.go()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 128), (6, 2, 64), (10, 2, 128)])
+def test_attention_whole_tiles_of_huge_values_behind_a_finite_mask(hq, hkv, d, dtype):
+    b = Batch([1500, 700], hq, hkv, d, 32, dtype, seed=44)
+    b.gain[:] = 1.0
+    for s in (0, 640, 1500 + 128):
+        b.bias[s:s + 192] = -250.0
+        b.v[s:s + 192] = synth.round_to(b.v[s:s + 192] * np.float32(2.0 ** 50), "bf16")
+    b.store()
+    b.go()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_huge_values_whose_weight_a_later_key_takes(dtype):
+    b = Batch([260, 500], 16, 8, 128, 64, dtype, seed=43)
+    b.gain[:] = 1.0
+    for s, n in ((0, 260), (260, 500)):
+        b.v[s:s + 70] = synth.round_to(b.v[s:s + 70] * np.float32(2.0 ** 40), "bf16")
+        b.bias[s + n - 60:s + n] += 120.0
+    b.store()
+    b.go()
+
+
 def test_attention_nan_in_a_live_row_reaches_its_own_request_only():
     b = Batch([50, 60], 4, 2, 64, 16, "bf16", seed=16)
     b.v[7, 0, :32] = np.nan            # request 0, KV head 0, dimensions 0..31
