@@ -365,7 +365,8 @@ class PagedDecodeBatch:
         """new_rows int32 [nreq] on the device: rows each request gets; k / v [rows, hkv*head_dim] their keys (rotated)
         and values by request, bias fp32 [rows] their importance; release uint8 [nreq] (or None): requests that give
         up what they hold first."""
-        slots = torch.empty(k.shape[0], dtype=torch.int32, device=k.device)
+        with torch.cuda.stream(stream):  # memory of the stream it is used on, so that no other one gets it meanwhile
+            slots = torch.empty(k.shape[0], dtype=torch.int32, device=k.device)
         self._pages(new_rows, release, slots, stream)
         tg.tg_kv4_store(self.cache, k, v, bias, slots, stream)
 

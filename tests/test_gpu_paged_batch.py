@@ -139,3 +139,29 @@ def test_training_chain_attention_backward_into_the_norm_and_rotation():
         dx, dw = K.qk_norm_rope_backward(rows, w, pos, 1e6, 1e-6, dy)
         np.testing.assert_allclose(got.cpu().numpy().reshape(dx.shape), dx, atol=2e-4 * np.abs(dx).max(), rtol=0)
         np.testing.assert_allclose(gw.cpu().numpy(), dw, atol=2e-4 * np.abs(dw).max(), rtol=0)
+
+
+def test_admission_on_a_side_stream_keeps_its_slots():
+    # the slots' memory must not go to other work of the current stream before the side stream has used it
+    n, hkv, d = 300, 2, 64
+    ones = torch.ones(4, device=DEV)
+    b = pipeline.PagedDecodeBatch(2, 400, 60, 16, hq=4, hkv=hkv, head_dim=d, head_gain=ones, head_temp=ones, device=DEV)
+    k, v = [torch.randint(-6, 7, (n, hkv * d), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    k[:, ::32] = v[:, ::32] = 6            # scale 1: the stored values are the nearest codes
+    new, bias = torch.tensor([n - 7, 7], dtype=torch.int32, device=DEV), torch.zeros(n, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)      # the side stream is behind
+    b.admit(new, k, v, bias, stream=side)
+    other = [torch.full((n,), -1, dtype=torch.int32, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert tg.tg_check_device_error() == 0 and all((t == -1).all() for t in other)
+    rows = torch.cat([torch.arange(n - 7), torch.arange(7)])
+    tables = b.tables.cpu()
+    slots = torch.cat([tables[0, rows[:n - 7] // 16], tables[1, rows[n - 7:] // 16]]) * 16 + rows % 16
+    got = [torch.empty(n, hkv * d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    tg.tg_kv4_load(b.cache, slots.to(torch.int32).to(DEV), *got)
+    for t, x in zip(got, (k, v)):
+        want = K.kv4_quantize(x.float().cpu().numpy().reshape(n, hkv, d))[0].reshape(n, -1)
+        np.testing.assert_array_equal(t.float().cpu().numpy(), want)
