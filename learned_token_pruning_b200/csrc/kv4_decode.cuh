@@ -40,8 +40,8 @@
 // Measured (16 + 8 heads of 128, bf16 queries, both kernels): 131137 rows of one request, pages
 // of 128: 40.6 us, 152 MB, 3.7 TB/s (57 % of a copy's 6.55); pages of 16: 45.7; a ragged batch of
 // 33 requests of up to 8321 rows, pages of 16: 48.3; 2129 rows: 10.4.  About 25 us of the 40
-// are the stream itself, the same when the cache sits in L2: 17.7 M warp instructions at 0.46 a
-// cycle and scheduler, with the logic pipe that takes the codes apart 43 % busy and the matrix
+// are the stream itself, the same when the cache sits in L2: 18.5 M warp instructions at 0.47 a
+// cycle and scheduler, with the logic pipe that takes the codes apart 44 % busy and the matrix
 // pipe 21 %.  Finite logits and units for any finite bias and value scale cost 0.5 us of them.  The other 15 are latency: the plan, the first page ids and keys, a run's
 // whole tiles, the pieces and the second kernel.
 // Tried: tiles of 32 keys, 41 .. 52 us; 16-byte copies by every lane in place of the bulk
