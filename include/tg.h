@@ -550,6 +550,7 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
  * slot = page * page_rows + row of the page.  In a row, dimensions 32g + 4r .. + 3 are
  * the 16-bit unit r * (head_dim / 32) + g, first dimension in the low bits; with
  * head_dim 128, rows 2 and 3 of every four have their two 32-byte halves swapped.
+ * A value is code times scale, whatever the scale's sign (tg_kv4_store writes none).
  * page_rows in {16, 32, 64, 128}, head_dim in {64, 128}, num_pages * page_rows < 2^31.
  */
 typedef struct {

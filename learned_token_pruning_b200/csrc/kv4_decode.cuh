@@ -61,6 +61,7 @@ namespace tg {
 constexpr int kKv4MaxGroup = 8;
 constexpr int kKv4Tile = 64;  // keys per unit of work: four matrix blocks whose chains overlap
 constexpr float kKv4Slack = 8.0f;    // a weight may exceed 1 by 2^8 before the running maximum follows
+constexpr uint32_t kKv4Magnitude = 0x7fffffffu;  // a float's bits without the sign: a value scale of the caller's may have one
 constexpr int kKv4WeightExp = 6;     // weight 1 times the largest value scale lands at 2^6 .. 2^7: 2^15 at most in fp16
 
 // Warps of one CTA (one CTA per SM): as many as registers hold.  bf16, 12 against 8: the ragged
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
         for (int b = 0; b < NB; ++b) {
           vs0[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + 2 * SL * b)) * shl16;
           vs1[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + D / 2 + 2 * SL * b)) * shl16;
-          vtop[b] = max(vtop[b], max(vs0[mt][b], vs1[mt][b]));
+          vtop[b] = max(vtop[b], max(vs0[mt][b] & kKv4Magnitude, vs1[mt][b] & kKv4Magnitude));
         }
       // The reference m and the unit of the weights move only when a logit passes m by
       // 2^8 or a value scale has a larger exponent (a warp vote; the first tile always does).
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           most[b] = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
           uint32_t least = 0xffffffffu;  // of this lane's scales that are not 0
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) least = min(least, min(vs0[mt][b] - 1, vs1[mt][b] - 1));
+          for (int mt = 0; mt < MT; ++mt) least = min(least, min((vs0[mt][b] & kKv4Magnitude) - 1, (vs1[mt][b] & kKv4Magnitude) - 1));
           apart |= real0 && most[b] - need[b] > 12 && (!near || most[b] - static_cast<int>(least >> 23) > 12);
         }
         apart = __any_sync(0xffffffffu, apart);
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
             for (int mt = 0; mt < MT; ++mt) {
               const float f0 = fmaxf(fmaxf(x[mt][0] - r0, x[mt][1] - r1), -300.0f);
               const float f1 = fmaxf(fmaxf(x[mt][2] - r0, x[mt][3] - r1), -300.0f);
-              u = max(u, max(min(static_cast<int>(vs0[mt][b] >> 23), 254) + static_cast<int>(ceilf(f0)),
-                             min(static_cast<int>(vs1[mt][b] >> 23), 254) + static_cast<int>(ceilf(f1))));
+              u = max(u, max(min(static_cast<int>(vs0[mt][b] >> 23 & 255u), 254) + static_cast<int>(ceilf(f0)),
+                             min(static_cast<int>(vs1[mt][b] >> 23 & 255u), 254) + static_cast<int>(ceilf(f1))));
             }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, s));
@@ -710,8 +711,9 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
               most[b] = u;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                if (vs0[mt][b] < 0x7f800000u) vs0[mt][b] = min(vs0[mt][b], cap);
-                if (vs1[mt][b] < 0x7f800000u) vs1[mt][b] = min(vs1[mt][b], cap);
+                const uint32_t abs0 = vs0[mt][b] & kKv4Magnitude, abs1 = vs1[mt][b] & kKv4Magnitude;
+                if (abs0 < 0x7f800000u) vs0[mt][b] += min(abs0, cap) - abs0;
+                if (abs1 < 0x7f800000u) vs1[mt][b] += min(abs1, cap) - abs1;
               }
             }
           }
