@@ -63,6 +63,7 @@ constexpr int kKv4Tile = 64;  // keys per unit of work: four matrix blocks whose
 constexpr float kKv4Slack = 8.0f;    // a weight may exceed 1 by 2^8 before the running maximum follows
 constexpr uint32_t kKv4Magnitude = 0x7fffffffu;  // a float's bits without the sign: a value scale of the caller's may have one
 constexpr int kKv4WeightExp = 6;     // weight 1 times the largest value scale lands at 2^6 .. 2^7: 2^15 at most in fp16
+constexpr int kKv4LeastUnit = kKv4WeightExp + 9;  // exponent (of a float) of the smallest unit: the factor, 2^118, times a weight, 2^8 at most, is a float
 
 // Warps of one CTA (one CTA per SM): as many as registers hold.  bf16, 12 against 8: the ragged
 // batch 47.7 / 50.1 us, 64 requests of 200 rows 13.5 / 15.1, 131137 rows 40.2 / 39.9.  With 8 heads
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.0f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) ex[b] = kKv4WeightExp + 1;  // from here on the weights' factor and its inverse are normal floats
+    for (int b = 0; b < NB; ++b) ex[b] = kKv4LeastUnit;
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       bool moved = t0 > m0 + kKv4Slack || t1 > m1 + kKv4Slack;
 #pragma unroll
       for (int b = 0; b < NB; ++b) moved |= static_cast<int>(vtop[b] >> 23) > ex[b];
+      bool far = false;  // a scale so far above its unit that a weight below the normal floats counts
       if (__any_sync(0xffffffffu, moved)) {
         const float tile0 = rows_max(t0), tile1 = rows_max(t1), n0 = fmaxf(m0, tile0), n1 = fmaxf(m1, tile1);
         const float d0 = n0 == m0 ? 0.0f : m0 - n0, d1 = n1 == m1 ? 0.0f : m1 - n1;
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
         bool apart = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          need[b] = max(ex[b] + (gone > -12.0f ? 0 : static_cast<int>(ceilf(gone))), kKv4WeightExp + 1);
+          need[b] = max(ex[b] + (gone > -12.0f ? 0 : static_cast<int>(ceilf(gone))), kKv4LeastUnit);
           int v = min(static_cast<int>(vtop[b] >> 23), 254);  // NaN scales (255) set no unit
           v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = max(v, __shfl_xor_sync(0xffffffffu, v, 8));
@@ -704,20 +706,14 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
             }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, s));
-            // scale times factor stays finite: above this a weight is 2^-103 at most
-            const uint32_t cap = u < 254 - 110 ? static_cast<uint32_t>(u + 110) << 23 : 0x7f800000u;
             need[b] = u;
             if (real0 && most[b] - u > 12) {
+              far |= most[b] - u > 90;
               most[b] = u;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const uint32_t abs0 = vs0[mt][b] & kKv4Magnitude, abs1 = vs1[mt][b] & kKv4Magnitude;
-                if (abs0 < 0x7f800000u) vs0[mt][b] += min(abs0, cap) - abs0;
-                if (abs1 < 0x7f800000u) vs1[mt][b] += min(abs1, cap) - abs1;
-              }
             }
           }
         }
+        far = __any_sync(0xffffffffu, far);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int nex = max(need[b], most[b]);
@@ -745,15 +741,21 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       // ---- weights, and their products with the values
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float p00 = kv4_ex2(x[mt][0] - use0), p01 = kv4_ex2(x[mt][1] - use1);
-        const float p10 = kv4_ex2(x[mt][2] - use0), p11 = kv4_ex2(x[mt][3] - use1);
+        float p00 = kv4_ex2(x[mt][0] - use0), p01 = kv4_ex2(x[mt][1] - use1);
+        float p10 = kv4_ex2(x[mt][2] - use0), p11 = kv4_ex2(x[mt][3] - use1);
+        if (far) {
+          p00 = exp2f(x[mt][0] - use0), p01 = exp2f(x[mt][1] - use1);
+          p10 = exp2f(x[mt][2] - use0), p11 = exp2f(x[mt][3] - use1);
+        }
         l0 += p00 + p10;
         l1 += p01 + p11;
         uint32_t pf[kSplit ? 2 : 1][NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float s0 = __uint_as_float(vs0[mt][b]) * fac[b], s1 = __uint_as_float(vs1[mt][b]) * fac[b];
-          const float w00 = p00 * s0, w01 = p01 * s0, w10 = p10 * s1, w11 = p11 * s1;
+          // the factor goes to the weight: a scale far above the unit (its weight far below 1) times
+          // the factor may pass the largest float, weight times factor cannot
+          const float s0 = __uint_as_float(vs0[mt][b]), s1 = __uint_as_float(vs1[mt][b]);
+          const float w00 = p00 * fac[b] * s0, w01 = p01 * fac[b] * s0, w10 = p10 * fac[b] * s1, w11 = p11 * fac[b] * s1;
           const uint32_t r0 = f16x2(w00, w01), r1 = f16x2(w10, w11);
           pf[0][b][0] = transpose8x8(r0);
           pf[0][b][1] = transpose8x8(r1);

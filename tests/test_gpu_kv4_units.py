@@ -22,6 +22,23 @@ SHAPES = [(16, 8, 128), (6, 2, 64), (8, 1, 128), (3, 1, 128)]
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("shift", [112, 116, 120, 123])
+def test_a_tiny_weight_times_a_huge_value_counts(shift, hq, hkv, d, dtype):
+    # weights of 2^-shift (normal floats) on values 2^shift times the others': equal contributions.  Logits of
+    # 120 in base 2 are off by at most 3 * 120 * 2^-24, which the tolerance of 1e-4 holds
+    b = Batch([150, 20], hq, hkv, d, 16, dtype, seed=51)
+    b.gain[:] = 1.0
+    b.temp[:] = 2.0 ** -4
+    for s, n in ((0, 150), (150, 20)):
+        few = s + np.arange(3, n, 17)
+        b.bias[few] = -shift * math.log(2)
+        b.v[few] = synth.round_to(np.clip(b.v[few], -2, 2) * np.float32(2.0 ** shift), "bf16")
+    b.store()
+    b.go()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
 def test_negative_scales_negate_what_the_codes_stand_for(hq, hkv, d, dtype):
     # the pools are the caller's memory, and a scale has a sign
     b = Batch([300, 70], hq, hkv, d, 16, dtype, seed=50)
