@@ -615,8 +615,9 @@ int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, v
  * bf16 or fp32 queries; head_dim in {64, 128}; at most 8 query heads per KV head; nreq
  * <= 4096, max_pages * page_rows <= 2^30, hkv * nreq * (max_pages * page_rows / 32 + 3)
  * < 2^31; nreq == 0 does nothing.  bf16 queries: weights rounded to 11 bits (fewer
- * where weight times value scale is below 2^-20 of the largest such product of two neighbouring heads), fp32 sums; fp32 queries:
- * queries and weights to 22 bits, fp32 sums.  A length that is negative or beyond the table
+ * where weight times value scale is below 2^-20 of the head's largest such product in the 32
+ * dimensions, or below 2^-137), fp32 sums; fp32 queries: queries and weights to 22 bits (weights:
+ * or 2^-31 of the largest product), fp32 sums.  A length that is negative or beyond the table
  * counts as 0, a page id outside the cache as page 0, and either sets the device error word.
  * The lengths are read on the device, so a captured call follows them.
  * Errors: TG_ERR_INVALID_ARG, TG_ERR_UNSUPPORTED, TG_ERR_SHAPE, TG_ERR_ALIGN (q and

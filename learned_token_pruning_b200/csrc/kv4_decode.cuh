@@ -21,9 +21,10 @@
 //   fp16 (11 bits; fp32 queries carry query and weights as two fp16 parts, 22 bits).
 //   Both factors meet a power of two that keeps them in fp16's range: the query one
 //   per head (its largest value lands at 2^8), the weights one per head and scale
-//   group (weight 1 times the largest value scale met so far lands at 2^6 .. 2^7; the
-//   running exponent moves with the softmax's reference, and follows the products where a huge
-//   row has next to no weight).
+//   group, the unit: the largest product of a weight and a value scale met so far lands at
+//   2^6 or above, so that products down to 2^-20 of it keep their 11 bits.  The unit moves with
+//   the softmax's reference and follows the products, not the scales: a huge row without weight
+//   must not cost the others their digits.
 //   The 8 columns hold HP heads (2, 4 or 8) times 8 / HP scale groups: with two
 //   heads, one B operand serves all four groups of D = 128.  A lane reads the
 //   accumulator columns of its own group and leaves the others.
@@ -60,10 +61,13 @@ namespace tg {
 
 constexpr int kKv4MaxGroup = 8;
 constexpr int kKv4Tile = 64;  // keys per unit of work: four matrix blocks whose chains overlap
-constexpr float kKv4Slack = 8.0f;    // a weight may exceed 1 by 2^8 before the running maximum follows
-constexpr uint32_t kKv4Magnitude = 0x7fffffffu;  // a float's bits without the sign: a value scale of the caller's may have one
-constexpr int kKv4WeightExp = 6;     // weight 1 times the largest value scale lands at 2^6 .. 2^7: 2^15 at most in fp16
-constexpr int kKv4LeastUnit = kKv4WeightExp + 9;  // exponent (of a float) of the smallest unit: the factor, 2^118, times a weight, 2^8 at most, is a float
+constexpr float kKv4Slack = 4.0f;   // a weight may exceed 1 by 2^4 before the running maximum follows
+constexpr int kKv4WeightExp = 10;   // a weight times a scale that is one unit lands at 2^10: 2^15 at most in fp16
+// A unit is set 2^3 above the largest product of a weight and a scale.  More makes moves rarer and
+// rounds coarser: 131137 rows (16 + 8 heads), value scales that spread by 2^4 (one standard deviation)
+// and biases of 6 between rows, 2^3 43.2 us, 2^6 42.9; ordinary rows 40.5 with both.
+constexpr int kKv4Over = 3;
+constexpr int kKv4LeastUnit = 14;   // the smallest unit: its factor, 2^123, times a weight, 2^4 at most, is a float
 
 // Warps of one CTA (one CTA per SM): as many as registers hold.  bf16, 12 against 8: the ragged
 // batch 47.7 / 50.1 us, 64 requests of 200 rows 13.5 / 15.1, 131137 rows 40.2 / 39.9.  With 8 heads
@@ -121,7 +125,17 @@ __device__ __forceinline__ float kv4_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float kv4_lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float exp_bits(int field) { return __uint_as_float(static_cast<uint32_t>(field) << 23); }
+// A unit (the exponent field of a float, kKv4LeastUnit .. 254), the factor that brings it to
+// 2^kKv4WeightExp, and that factor's inverse.  Both are normal floats.
+__device__ __forceinline__ float factor_of(int unit) { return exp_bits(254 + kKv4WeightExp - unit); }
+__device__ __forceinline__ int unit_of(float factor) { return 254 + kKv4WeightExp - static_cast<int>(__float_as_uint(factor) >> 23); }
+__device__ __forceinline__ float inverse_of(float factor) { return exp_bits(unit_of(factor) - kKv4WeightExp); }
 
 // N neighbouring words of shared memory.  Plain loads, like the matrix instructions below
 // without `volatile`: the compiler may move them past one another, which is what
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
   float o[NG][2][4];
   float bias_most = 0.0f;  // gain times a bias up to this is finite in base 2
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, a0 = 0.0f, a1 = 0.0f, g0 = 0.0f, g1 = 0.0f;
-  int ex[NB];
+  float fac0[NB], fac1[NB];  // the weights' factors
 
   auto begin = [&]() {  // a new (request, head): its query, factors, and empty sums
     const int h0 = cg * group;
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.0f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) ex[b] = kKv4LeastUnit;
+    for (int b = 0; b < NB; ++b) fac0[b] = factor_of(hd < group ? kKv4LeastUnit : 254), fac1[b] = factor_of(hd + 1 < group ? kKv4LeastUnit : 254);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -486,11 +500,12 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (g % SL != slot) continue;
-      const float unit = exp_bits(ex[g / SL] - kKv4WeightExp);  // the inverse of the weights' factor
+      const float back0 = inverse_of(fac0[g / SL]), back1 = inverse_of(fac1[g / SL]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (hd + c >= group) continue;
         const float f = c ? f1 : f0;
+        const float unit = c ? back1 : back0;
         const float y0 = o[g][0][c] * f * unit, y1 = o[g][0][c + 2] * f * unit;
         const float y2 = o[g][1][c] * f * unit, y3 = o[g][1][c + 2] * f * unit;
         const int at = 32 * g + 4 * n8;
@@ -648,78 +663,52 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
         __syncwarp();
       }
       uint32_t vs0[MT][NB], vs1[MT][NB];  // bf16 value scales of this lane's groups, as fp32 bits
-      uint32_t vtop[NB];
+      float vtop[NB];  // largest magnitude; NaN is passed over
 #pragma unroll
-      for (int b = 0; b < NB; ++b) vtop[b] = 0;
+      for (int b = 0; b < NB; ++b) vtop[b] = 0.0f;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           vs0[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + 2 * SL * b)) * shl16;
           vs1[mt][b] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(smem + wbase + mt * D + D / 2 + 2 * SL * b)) * shl16;
-          vtop[b] = max(vtop[b], max(vs0[mt][b] & kKv4Magnitude, vs1[mt][b] & kKv4Magnitude));
+          vtop[b] = fmax3(vtop[b], fabsf(__uint_as_float(vs0[mt][b])), fabsf(__uint_as_float(vs1[mt][b])));
         }
-      // The reference m and the unit of the weights move only when a logit passes m by
-      // 2^8 or a value scale has a larger exponent (a warp vote; the first tile always does).
+      // The reference m and the units of the weights move only when a weight would pass
+      // 2^kKv4Slack or a value scale is twice a unit (a warp vote; the first tile always does).
       bool moved = t0 > m0 + kKv4Slack || t1 > m1 + kKv4Slack;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) moved |= static_cast<int>(vtop[b] >> 23) > ex[b];
+      for (int b = 0; b < NB; ++b) moved |= vtop[b] * fmaxf(fac0[b], fac1[b]) >= exp_bits(128 + kKv4WeightExp);
       bool far = false;  // a scale so far above its unit that a weight below the normal floats counts
       if (__any_sync(0xffffffffu, moved)) {
         const float tile0 = rows_max(t0), tile1 = rows_max(t1), n0 = fmaxf(m0, tile0), n1 = fmaxf(m1, tile1);
         const float d0 = n0 == m0 ? 0.0f : m0 - n0, d1 = n1 == m1 ? 0.0f : m1 - n1;
         l0 *= kv4_ex2(d0);
         l1 *= kv4_ex2(d1);
-        // The unit follows the largest value scale, unless that one's weight makes it more than 2^12
-        // too large for what is summed (a huge row behind a finite mask): then the largest product
-        // of a weight and a scale, or what the sums so far come to under the new reference.  The
-        // products are looked at only where scales are that far apart, or all of the tile's
-        // weights small.
-        const bool real0 = hd < group, real1 = hd + 1 < group, near = (real0 && tile0 == n0) || (real1 && tile1 == n1);
-        const float gone = fmaxf(fmaxf(real0 ? d0 : -300.0f, real1 ? d1 : -300.0f), -300.0f);
-        int need[NB], most[NB];
-        bool apart = false;
+        // A unit falls with its head's sums as the reference rises, and rises to 2^kKv4Over times
+        // the tile's largest product of a weight and a scale: so it is never further than that (and
+        // a rounding up) above the largest product so far, whatever came before, and scales
+        // have to grow that much before the next tile moves it.
+        const bool real0 = hd < group, real1 = hd + 1 < group;
+        const int fall0 = static_cast<int>(floorf(fmaxf(d0, -300.0f))), fall1 = static_cast<int>(floorf(fmaxf(d1, -300.0f)));
+        const float r0 = fmaxf(n0, -FLT_MAX), r1 = fmaxf(n1, -FLT_MAX);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          need[b] = max(ex[b] + (gone > -12.0f ? 0 : static_cast<int>(ceilf(gone))), kKv4LeastUnit);
-          int v = min(static_cast<int>(vtop[b] >> 23), 254);  // NaN scales (255) set no unit
-          v = max(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = max(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          most[b] = max(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          uint32_t least = 0xffffffffu;  // of this lane's scales that are not 0
+          float u0 = -300.0f, u1 = -300.0f;  // base 2
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) least = min(least, min((vs0[mt][b] & kKv4Magnitude) - 1, (vs1[mt][b] & kKv4Magnitude) - 1));
-          apart |= real0 && most[b] - need[b] > 12 && (!near || most[b] - static_cast<int>(least >> 23) > 12);
-        }
-        apart = __any_sync(0xffffffffu, apart);
-        if (apart) {
-          const float r0 = real0 ? fmaxf(n0, -FLT_MAX) : INFINITY, r1 = real1 ? fmaxf(n1, -FLT_MAX) : INFINITY;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            int u = need[b];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const float f0 = fmaxf(fmaxf(x[mt][0] - r0, x[mt][1] - r1), -300.0f);
-              const float f1 = fmaxf(fmaxf(x[mt][2] - r0, x[mt][3] - r1), -300.0f);
-              u = max(u, max(min(static_cast<int>(vs0[mt][b] >> 23 & 255u), 254) + static_cast<int>(ceilf(f0)),
-                             min(static_cast<int>(vs1[mt][b] >> 23 & 255u), 254) + static_cast<int>(ceilf(f1))));
-            }
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, s));
-            need[b] = u;
-            if (real0 && most[b] - u > 12) {
-              far |= most[b] - u > 90;
-              most[b] = u;
-            }
+          for (int mt = 0; mt < MT; ++mt) {
+            const float e0 = kv4_lg2(fabsf(__uint_as_float(vs0[mt][b]))), e1 = kv4_lg2(fabsf(__uint_as_float(vs1[mt][b])));
+            u0 = fmax3(u0, x[mt][0] - r0 + e0, x[mt][2] - r0 + e1);
+            u1 = fmax3(u1, x[mt][1] - r1 + e0, x[mt][3] - r1 + e1);
           }
-        }
-        far = __any_sync(0xffffffffu, far);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int nex = max(need[b], most[b]);
-          const float de = static_cast<float>(ex[b] - nex);
-          const float c0 = kv4_ex2(d0 + de), c1 = kv4_ex2(d1 + de);
-          ex[b] = nex;
+          u0 = rows_max(u0), u1 = rows_max(u1);
+          const int old0 = unit_of(fac0[b]), old1 = unit_of(fac1[b]);
+          const int new0 = real0 ? max(max(old0 + fall0, kKv4LeastUnit), 127 + min(kKv4Over + static_cast<int>(ceilf(fminf(u0, 128.0f))), 127)) : 254;
+          const int new1 = real1 ? max(max(old1 + fall1, kKv4LeastUnit), 127 + min(kKv4Over + static_cast<int>(ceilf(fminf(u1, 128.0f))), 127)) : 254;
+          far |= static_cast<int>(__float_as_uint(vtop[b]) >> 23) - min(new0, new1) > 90;
+          const float c0 = kv4_ex2(d0 + static_cast<float>(old0 - new0)), c1 = kv4_ex2(d1 + static_cast<float>(old1 - new1));
+          fac0[b] = factor_of(new0);
+          fac1[b] = factor_of(new1);
 #pragma unroll
           for (int g = b * SL; g < (b + 1) * SL && g < NG; ++g)
 #pragma unroll
@@ -730,13 +719,11 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
               o[g][j][3] *= c1;
             }
         }
+        far = __any_sync(0xffffffffu, far);
         m0 = n0;
         m1 = n1;
       }
       const float use0 = m0 == -INFINITY ? 0.0f : m0, use1 = m1 == -INFINITY ? 0.0f : m1;
-      float fac[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) fac[b] = exp_bits(254 + kKv4WeightExp - ex[b]);  // 2^(127 + kKv4WeightExp - ex)
 
       // ---- weights, and their products with the values
 #pragma unroll
@@ -755,7 +742,7 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           // the factor goes to the weight: a scale far above the unit (its weight far below 1) times
           // the factor may pass the largest float, weight times factor cannot
           const float s0 = __uint_as_float(vs0[mt][b]), s1 = __uint_as_float(vs1[mt][b]);
-          const float w00 = p00 * fac[b] * s0, w01 = p01 * fac[b] * s0, w10 = p10 * fac[b] * s1, w11 = p11 * fac[b] * s1;
+          const float w00 = p00 * fac0[b] * s0, w01 = p01 * fac1[b] * s0, w10 = p10 * fac0[b] * s1, w11 = p11 * fac1[b] * s1;
           const uint32_t r0 = f16x2(w00, w01), r1 = f16x2(w10, w11);
           pf[0][b][0] = transpose8x8(r0);
           pf[0][b][1] = transpose8x8(r1);
