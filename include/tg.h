@@ -480,7 +480,9 @@ int tg_linear(const void* x, int64_t ldx, const void* w, void* y, int64_t ldy, i
  * request given rows) the call can be repeated with the same result.  A request
  * that cannot be met (too few pages, a table or slots too short, a negative or
  * too large length) sets the device error word (TG_ERR_DEVICE_CHECK), and then
- * nothing changes but slots (all -1) and row_start (all 0).
+ * nothing changes but slots (all -1) and row_start (all 0).  A page id below 0, or one whose
+ * slot passes 2^31 - 1, gives its rows slot -1 and sets the error word too, but is met
+ * only as the slots are written: tables, free list and lengths are then those of the call.
  * Any page_rows >= 1; nreq <= 4096, max_pages * page_rows and nslots <= 2^30; nreq == 0
  * only marks the slots.  Errors: TG_ERR_INVALID_ARG (null pointer, sizes < 0, page_rows
  * or max_pages < 1), TG_ERR_UNSUPPORTED (past those limits).

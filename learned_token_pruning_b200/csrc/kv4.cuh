@@ -62,6 +62,7 @@ struct PageTableParams {
   const uint8_t* release;  // or null
   int32_t nreq;
   int32_t page_rows;
+  uint32_t last_page;  // the last one with a slot of 31 bits
   int32_t* tables;
   int32_t max_pages;
   int32_t* free_pages;
@@ -235,8 +236,13 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
 #pragma unroll
     for (int k = 0; k < kTabTimes; ++k) {
       const int i = i0 + 32 * k;
-      if (id[k] < 0 && off[k] >= 0) raise_error(kErrPageTable, 4);
-      if (k < times && i < p.nslots) p.slots[i] = id[k] < 0 ? -1 : id[k] * p.page_rows + off[k];
+      // any page ids and page sizes: up to the last page the product fits 32 bits, and past 2^31 - 1 it is negative
+      int32_t slot = static_cast<int32_t>(static_cast<uint32_t>(id[k]) * p.page_rows + off[k]);
+      if (static_cast<uint32_t>(id[k]) > p.last_page || slot < 0) {
+        slot = -1;
+        if (off[k] >= 0) raise_error(kErrPageTable, 4);
+      }
+      if (k < times && i < p.nslots) p.slots[i] = slot;
     }
   }
   for (int i = t0; i <= p.nreq; i += step) {

@@ -1969,6 +1969,7 @@ int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* 
   p.release = release;
   p.nreq = nreq;
   p.page_rows = page_rows;
+  p.last_page = INT32_MAX / page_rows;
   p.tables = tables;
   p.max_pages = max_pages;
   p.free_pages = free_pages;
