@@ -449,9 +449,12 @@ __global__ void __launch_bounds__(256) k_kv4_store(const Kv4RowsParams p) {
       if (t.li == 0) raise_error(kErrKvSlot, 1);
       slot[u] = -1;
     }
-    // max / 6 rounded to bf16 by way of fp32, which meets no false tie: an fp32 quotient by 6
-    // that is not a bf16 tie stays an fp32 step away from one, and for a bf16 maximum the
-    // product with 1/6 (2^-25 off) is on a tie where the quotient is and 2^-12 away elsewhere
+    // max / 6 rounded to bf16 by way of fp32, which must meet no false tie.  The product with 1/6
+    // (2^-25 off) is less than a step from the quotient.  For a bf16 maximum it is on a tie where
+    // the quotient is and 2^-12 away elsewhere.  For an fp32 maximum the remainder's sign
+    // says which side of it the quotient lies on: a product above it goes a step down, and the last
+    // bit is set where there is a remainder, so that only an exact quotient is on a tie (below the
+    // smallest normal number an fp32 quotient rounded to nearest can fall on one).
     uint32_t top = top8(raw[u]);
     float sixth;
     if constexpr (kW == 1) {
@@ -462,7 +465,10 @@ __global__ void __launch_bounds__(256) k_kv4_store(const Kv4RowsParams p) {
     } else {
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      sixth = __uint_as_float(top) / 6.0f;
+      const float max = __uint_as_float(top);
+      sixth = max * (1.0f / 6.0f);
+      const float rest = fmaf(sixth, -6.0f, max);
+      sixth = __uint_as_float((__float_as_uint(sixth) - (rest < 0.0f)) | (rest != 0.0f));
     }
     const bool finite = top < 0x7f800000u;
     const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? sixth : __uint_as_float(0x7fffffffu));
