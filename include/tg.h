@@ -493,6 +493,17 @@ int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* 
                    int32_t* row_start, void* stream);
 
 /*
+ * tg_page_tables for a step of one token a request, some of them idle: new_rows[r] is 0 or 1 (more
+ * is refused as a request that cannot be met), and slots, int32 [nreq], are by request:
+ * slots[r] is the slot of request r's new row, -1 where it has none, so that row r of a batch's
+ * keys and values goes to slots[r].  row_start as there, or NULL.  Else as tg_page_tables.
+ */
+int tg_page_tables_by_request(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                              int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages,
+                              int32_t free_cap, const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out,
+                              int32_t* slots, int32_t* row_start, void* stream);
+
+/*
  * Per-head RMSNorm of q and k and the rotation to their positions in one pass
  * ([R] §4.1: RoPE above the gate at the original positions; the step between
  * the projections and attention in tg_pruned_prefill_layer, for callers that

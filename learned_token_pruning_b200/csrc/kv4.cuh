@@ -72,7 +72,8 @@ struct PageTableParams {
   int32_t* n_free_out;
   int32_t* slots;
   int32_t nslots;
-  int32_t* row_start;
+  int32_t* row_start;  // null only where slots are by request
+  bool by_request;     // one new row at most: slots[r] is request r's
 };
 
 __host__ __device__ constexpr size_t page_table_smem(int nreq) { return static_cast<size_t>(4 * nreq + 3) * 4; }
@@ -87,6 +88,17 @@ __device__ __forceinline__ int find_request(const int32_t* start, int n, int32_t
     else hi = mid - 1;
   }
   return lo;
+}
+
+// The slot of row `row` of a page, -1 for a bad page id (reported) and for none (both -1).  Any ids
+// and page sizes: up to the last page the product fits 32 bits, and past 2^31 - 1 it is negative.
+__device__ __forceinline__ int32_t page_slot(const PageTableParams& p, int32_t id, int32_t row) {
+  int32_t slot = static_cast<int32_t>(static_cast<uint32_t>(id) * p.page_rows + row);
+  if (static_cast<uint32_t>(id) > p.last_page || slot < 0) {
+    slot = -1;
+    if (row >= 0) raise_error(kErrPageTable, 4);
+  }
+  return slot;
 }
 
 __device__ __forceinline__ void block_scan3(int64_t (&v)[3], int64_t (*s_warp)[3], int64_t (&before)[3],
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
     if (i < per && r < p.nreq) {
       int64_t l = p.lens[r];
       const int64_t n = p.new_rows[r];
-      if (l < 0 || l > most || n < 0) bad = true;
+      if (l < 0 || l > most || n < 0 || (p.by_request && n > 1)) bad = true;
       else {
         if (p.release && p.release[r]) {
           back[i] = static_cast<int32_t>((l + P - 1) / P);
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
   if (refuse) {
     if (t0 == 0) raise_error(kErrPageTable, s_bad ? 1u : (total[1] > nf + total[0] ? 2u : 3u));
     for (int i = t0; i < p.nslots; i += step) p.slots[i] = -1;
-    for (int i = t0; i <= p.nreq; i += step) p.row_start[i] = 0;
+    for (int i = t0; p.row_start && i <= p.nreq; i += step) p.row_start[i] = 0;
     for (int i = t0; i < p.nreq && p.lens_out != p.lens; i += step) p.lens_out[i] = p.lens[i];
     if (t0 == 0) *p.n_free_out = static_cast<int32_t>(nf);
     return;
@@ -207,6 +219,13 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
     const int first = (s_len[r] + p.page_rows - 1) / p.page_rows;
     p.tables[static_cast<int64_t>(r) * p.max_pages + first + (i - s_take[r])] = __ldcg(p.free_pages + (top - 1 - i));
   }
+  // the id of page `page` of request r: pages taken in this call are read off the free list
+  // (another thread writes the table)
+  auto page_id = [&](int r, int32_t page) {
+    const int32_t held = (s_len[r] + p.page_rows - 1) / p.page_rows;
+    return __ldcg(page < held ? p.tables + static_cast<int64_t>(r) * p.max_pages + page
+                              : p.free_pages + (top - 1 - (s_take[r] + page - held)));
+  };
   // A warp takes 32 neighbouring slots up to eight times in a row, as often as it takes to go
   // round once: one search for the first row's request, then short walks, and the page ids a
   // lane needs on their way together.  129828 slots of 1000 requests, 16 CTAs: eight times
@@ -214,7 +233,11 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
   // requests as slots: 15.1 and 9.0.
   const int lane = threadIdx.x & 31;
   const int times = max(1, min(kTabTimes, (p.nslots + step - 1) / step));
-  for (int c = t0 >> 5; static_cast<int64_t>(c) * times * 32 < p.nslots; c += step >> 5) {
+  for (int r = t0; p.by_request && r < p.nreq; r += step) {
+    const int32_t page = s_len[r] / p.page_rows;
+    p.slots[r] = s_rows[r + 1] == s_rows[r] ? -1 : page_slot(p, page_id(r, page), s_len[r] - page * p.page_rows);
+  }
+  for (int c = t0 >> 5; !p.by_request && static_cast<int64_t>(c) * times * 32 < p.nslots; c += step >> 5) {
     const int i0 = c * times * 32 + lane;
     int r = i0 < nrows ? find_request(s_rows, p.nreq, i0) : 0;
     int32_t id[kTabTimes], off[kTabTimes];
@@ -226,27 +249,20 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
       if (k < times && i < nrows) {
         while (s_rows[r + 1] <= i) ++r;
         const int32_t at = s_len[r] + (i - s_rows[r]);
-        const int32_t page = at / p.page_rows, held = (s_len[r] + p.page_rows - 1) / p.page_rows;
+        const int32_t page = at / p.page_rows;
         off[k] = at - page * p.page_rows;
-        // pages taken in this call are read off the free list (another thread writes the table)
-        id[k] = __ldcg(page < held ? p.tables + static_cast<int64_t>(r) * p.max_pages + page
-                                   : p.free_pages + (top - 1 - (s_take[r] + page - held)));
+        id[k] = page_id(r, page);
       }
     }
 #pragma unroll
     for (int k = 0; k < kTabTimes; ++k) {
       const int i = i0 + 32 * k;
-      // any page ids and page sizes: up to the last page the product fits 32 bits, and past 2^31 - 1 it is negative
-      int32_t slot = static_cast<int32_t>(static_cast<uint32_t>(id[k]) * p.page_rows + off[k]);
-      if (static_cast<uint32_t>(id[k]) > p.last_page || slot < 0) {
-        slot = -1;
-        if (off[k] >= 0) raise_error(kErrPageTable, 4);
-      }
+      const int32_t slot = page_slot(p, id[k], off[k]);
       if (k < times && i < p.nslots) p.slots[i] = slot;
     }
   }
   for (int i = t0; i <= p.nreq; i += step) {
-    p.row_start[i] = s_rows[i];
+    if (p.row_start) p.row_start[i] = s_rows[i];
     if (i < p.nreq) p.lens_out[i] = s_len[i] + (s_rows[i + 1] - s_rows[i]);
   }
   if (t0 == 0) *p.n_free_out = top - ntake;

@@ -1951,13 +1951,15 @@ int tg_qk_norm_rope_backward(const void* q, int64_t ldq, const void* k, int64_t 
 // ---------------------------------------------------------------------------
 // The paged 4-bit cache
 // ---------------------------------------------------------------------------
-int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
-                   int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
-                   const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* slots, int32_t nslots,
-                   int32_t* row_start, void* stream) {
+}  // extern "C"
+
+static int page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                       int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
+                       const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* slots, int32_t nslots,
+                       int32_t* row_start, bool by_request, void* stream) {
   if (nreq < 0 || nslots < 0 || free_cap < 0 || page_rows < 1 || max_pages < 1)
     return fail(TG_ERR_INVALID_ARG, "bad sizes");
-  if (!n_free || !n_free_out || !row_start || (nslots > 0 && !slots) || (free_cap > 0 && !free_pages))
+  if (!n_free || !n_free_out || (!row_start && !by_request) || (nslots > 0 && !slots) || (free_cap > 0 && !free_pages))
     return fail(TG_ERR_INVALID_ARG, "null pointer");
   if (nreq > 0 && (!lens || !new_rows || !tables || !lens_out)) return fail(TG_ERR_INVALID_ARG, "null pointer");
   if (nreq > tg::kTabMaxReq) return fail(TG_ERR_UNSUPPORTED, "at most %d requests", tg::kTabMaxReq);
@@ -1980,6 +1982,7 @@ int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* 
   p.slots = slots;
   p.nslots = nslots;
   p.row_start = row_start;
+  p.by_request = by_request;
   const size_t smem = tg::page_table_smem(nreq);
   int rc = set_smem(tg::k_page_tables, tg::page_table_smem(tg::kTabMaxReq));
   if (rc) return rc;
@@ -2001,6 +2004,24 @@ int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* 
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tg::k_page_tables, p);
   if (e != cudaSuccess) return fail(TG_ERR_CUDA, "k_page_tables launch: %s", cudaGetErrorString(e));
   return check_launch("k_page_tables");
+}
+
+extern "C" {
+
+int tg_page_tables(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                   int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages, int32_t free_cap,
+                   const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* slots, int32_t nslots,
+                   int32_t* row_start, void* stream) {
+  return page_tables(lens, new_rows, release, nreq, page_rows, tables, max_pages, free_pages, free_cap, n_free, lens_out,
+                     n_free_out, slots, nslots, row_start, false, stream);
+}
+
+int tg_page_tables_by_request(const int32_t* lens, const int32_t* new_rows, const uint8_t* release, int32_t nreq,
+                              int32_t page_rows, int32_t* tables, int32_t max_pages, int32_t* free_pages,
+                              int32_t free_cap, const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out,
+                              int32_t* slots, int32_t* row_start, void* stream) {
+  return page_tables(lens, new_rows, release, nreq, page_rows, tables, max_pages, free_pages, free_cap, n_free, lens_out,
+                     n_free_out, slots, nreq, row_start, true, stream);
 }
 
 }  // extern "C"

@@ -324,8 +324,15 @@ class PagedDecodeBatch:
 
       admit()  the kept rows of new prompts enter the cache (and finished
                requests give their pages back): page tables, then the rows;
-      step()   one new token for every request: page tables, q/k norm and
+      step()   one new token for every live request: page tables, q/k norm and
                rotation, the new rows into the cache, attention over it.
+
+    live (int32 [nreq] on the device) says which requests take part in a step: 1, or 0 for an
+    idle one, which gets no row and keeps what it holds (its row of out is then of no meaning, and
+    its q and k in qkv are rotated like the others').  admit() makes requests that
+    get rows live and those left without any idle; a program sets the others itself, as
+    for a request that has ended or holds max_rows: one more row for that would be refused
+    for the whole batch.
 
     A step is five library kernels on one stream and can be captured: the same
     graph then serves every following step."""
@@ -343,7 +350,7 @@ class PagedDecodeBatch:
         self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=i32, device=dev)   # page 0 is taken first
         self.n_free = torch.full((1,), num_pages, dtype=i32, device=dev)
         self.row_start = torch.zeros(nreq + 1, dtype=i32, device=dev)
-        self.one = torch.ones(nreq, dtype=i32, device=dev)
+        self.live = torch.zeros(nreq, dtype=i32, device=dev)
         self.slots = torch.empty(nreq, dtype=i32, device=dev)
         # one step's inputs and result: [q | k | v] of the projection, positions, temperature ratios
         self.qkv = torch.zeros(nreq, (hq + 2 * hkv) * head_dim, dtype=dtype, device=dev)
@@ -357,24 +364,25 @@ class PagedDecodeBatch:
         self.ws = torch.zeros(tg.kv4_decode_workspace_bytes(hq, hkv, head_dim), dtype=torch.uint8, device=dev)
         self._graph = None
 
-    def _pages(self, new_rows, release, slots, stream):
-        tg.tg_page_tables(self.lens, new_rows, release, self.page_rows, self.tables, self.free_pages, self.n_free, self.lens,
-                          self.n_free, slots, self.row_start, stream)
-
     def admit(self, new_rows, k, v, bias, release=None, stream=None):
         """new_rows int32 [nreq] on the device: rows each request gets; k / v [rows, hkv*head_dim] their keys (rotated)
         and values by request, bias fp32 [rows] their importance; release uint8 [nreq] (or None): requests that give
         up what they hold first."""
         with torch.cuda.stream(stream):  # memory of the stream it is used on, so that no other one gets it meanwhile
             slots = torch.empty(k.shape[0], dtype=torch.int32, device=k.device)
-        self._pages(new_rows, release, slots, stream)
+        tg.tg_page_tables(self.lens, new_rows, release, self.page_rows, self.tables, self.free_pages, self.n_free, self.lens,
+                          self.n_free, slots, self.row_start, stream)
         tg.tg_kv4_store(self.cache, k, v, bias, slots, stream)
+        with torch.cuda.stream(stream):  # a refused call has no row starts past 0
+            met = (new_rows > 0) & (self.row_start[-1] > 0)
+            self.live.copy_((self.lens > 0) & ((self.live != 0) | met))
 
     def step(self, stream=None):
-        """One token for every request from self.qkv, self.pos and self.ratio; the result is left in self.out.  q and k
-        are normalised and rotated in place."""
+        """One token for every live request from self.qkv, self.pos and self.ratio; the result is left in self.out.  q and
+        k are normalised and rotated in place."""
         wq, wk, eps, theta, norm = self.norm
-        self._pages(self.one, None, self.slots, stream)
+        tg.tg_page_tables_by_request(self.lens, self.live, None, self.page_rows, self.tables, self.free_pages, self.n_free,
+                                     self.lens, self.n_free, self.slots, self.row_start, stream)
         tg.tg_qk_norm_rope(self.q, self.k, self.head_dim, self.pos, wq, wk, eps, theta, self.q, self.k, qk_norm=norm,
                            stream=stream)
         tg.tg_kv4_store(self.cache, self.k, self.v, None, self.slots, stream)

@@ -87,6 +87,7 @@ SIGNATURES = {
     "tg_gather_prefill_layer": (_INT, [ctypes.POINTER(LayerWeights), ctypes.POINTER(LayerShape), _INT, _P, _I64, _P,
                                        _I64, _P, _P, _I64, _F, _P, _P, _P, _P, _P, _SZ, _P]),
     "tg_page_tables": (_INT, [_P, _P, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P]),
+    "tg_page_tables_by_request": (_INT, [_P, _P, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _P]),
     "tg_qk_norm_rope": (_INT, [_P, _I64, _P, _I64, _INT, _I64, _I32, _I32, _I32, _P, _P, _P, _I32, _F, _F, _P, _I64, _P,
                                _I64, _P]),
     "tg_qk_norm_rope_backward": (_INT, [_P, _I64, _P, _I64, _INT, _I64, _I32, _I32, _I32, _P, _P, _P, _I32, _F, _F, _P,
@@ -443,6 +444,20 @@ def tg_page_tables(lens, new_rows, release, page_rows: int, tables, free_pages, 
                               _arg(n_free_out, "n_free_out", i32, dev, 1), _arg(slots, "slots", i32, dev), slots.numel(),
                               _arg(row_start, "row_start", i32, dev, n + 1), _on(stream, dev))
     _check("tg_page_tables", rc)
+
+
+def tg_page_tables_by_request(lens, new_rows, release, page_rows: int, tables, free_pages, n_free, lens_out, n_free_out,
+                              slots, row_start=None, stream=None):
+    """tg_page_tables for new_rows of 0 or 1; slots int32 [nreq] by request (-1: no row), row_start may be None."""
+    n, i32, dev = lens.numel(), _I32T, _here()
+    _need(tables.dim() == 2 and tables.shape[0] == n, "tables must be [nreq, max_pages]")
+    rc = lib().tg_page_tables_by_request(
+        _arg(lens, "lens", i32, dev), _arg(new_rows, "new_rows", i32, dev, n), _arg(release, "release", _U8T, dev, n), n,
+        page_rows, _arg(tables, "tables", i32, dev), tables.shape[1], _arg(free_pages, "free_pages", i32, dev),
+        free_pages.numel(), _arg(n_free, "n_free", i32, dev, 1), _arg(lens_out, "lens_out", i32, dev, n),
+        _arg(n_free_out, "n_free_out", i32, dev, 1), _arg(slots, "slots", i32, dev, n),
+        _arg(row_start, "row_start", i32, dev, n + 1), _on(stream, dev))
+    _check("tg_page_tables_by_request", rc)
 
 
 def tg_qk_norm_rope(q, k, head_dim: int, pos, w_q, w_k, norm_eps: float, rope_theta: float, q_out, k_out,
