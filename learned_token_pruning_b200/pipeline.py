@@ -331,8 +331,9 @@ class PagedDecodeBatch:
     idle one, which gets no row and keeps what it holds (its row of out is then of no meaning, and
     its q and k in qkv are rotated like the others').  admit() makes requests that
     get rows live and those left without any idle; a program sets the others itself, as
-    for a request that has ended or holds max_rows: one more row for that would be refused
-    for the whole batch.
+    for a request that has ended or holds max_rows.  A step that cannot be met (a live request at
+    max_rows, too few pages) gives nobody a row, leaves in out what the rows of before come to, and sets
+    the device error word (tg_check_device_error).
 
     A step is five library kernels on one stream and can be captured: the same
     graph then serves every following step."""
@@ -391,12 +392,14 @@ class PagedDecodeBatch:
         return self.out
 
     def capture(self):
-        """Record step() without taking one: lengths, tables and the free list are put back afterwards, so the first
-        replay is the next step.  (The eager call before the recording sets the kernels' attributes up.)"""
-        state = [t.clone() for t in (self.lens, self.tables, self.free_pages, self.n_free, self.qkv)]
+        """Record step() without taking one: the first replay is the next step.  The eager call before the recording
+        sets the kernels' attributes up; with no request live it takes no row, on a full batch too, and what it does to
+        qkv is put back."""
+        live, qkv = self.live.clone(), self.qkv.clone()
+        self.live.zero_()
         self.step()
-        for t, old in zip((self.lens, self.tables, self.free_pages, self.n_free, self.qkv), state):
-            t.copy_(old)
+        self.live.copy_(live)
+        self.qkv.copy_(qkv)
         torch.cuda.synchronize(self.out.device)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):

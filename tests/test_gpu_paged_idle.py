@@ -134,3 +134,15 @@ def test_a_refused_admission_leaves_the_live_requests_as_they_were():
     with pytest.raises(tg.TokenGateError):
         tg.tg_check_device_error()
     assert b.live.tolist() == [1, 0, 0] and b.lens.tolist() == [16, 0, 16]
+
+
+def test_capturing_a_full_batch_reports_nothing_and_changes_nothing():
+    b = pipeline.PagedDecodeBatch(2, 32, 3, 16, hq=4, hkv=2, head_dim=64, head_gain=torch.ones(4, device=DEV),
+                                  head_temp=torch.ones(4, device=DEV), device=DEV)
+    kv = torch.randn(48, 128, device=DEV, dtype=torch.bfloat16)
+    b.admit(torch.tensor([32, 16], dtype=torch.int32, device=DEV), kv, kv, torch.zeros(48, device=DEV))
+    state = [t.clone() for t in (b.lens, b.tables, b.free_pages, b.n_free, b.qkv, b.cache.k_codes, b.cache.bias)]
+    b.capture()
+    assert tg.tg_check_device_error() == 0
+    for t, old in zip((b.lens, b.tables, b.free_pages, b.n_free, b.qkv, b.cache.k_codes, b.cache.bias), state):
+        assert torch.equal(t, old)
