@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(256) k_kv4_store(const Kv4RowsParams p) {
     } else {
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float max = __uint_as_float(top);
-      sixth = max * (1.0f / 6.0f);
-      const float rest = fmaf(sixth, -6.0f, max);
+      const float largest = __uint_as_float(top);
+      sixth = largest * (1.0f / 6.0f);
+      const float rest = fmaf(sixth, -6.0f, largest);
       sixth = __uint_as_float((__float_as_uint(sixth) - (rest < 0.0f)) | (rest != 0.0f));
     }
     const bool finite = top < 0x7f800000u;

@@ -742,7 +742,10 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
           // the factor goes to the weight: a scale far above the unit (its weight far below 1) times
           // the factor may pass the largest float, weight times factor cannot
           const float s0 = __uint_as_float(vs0[mt][b]), s1 = __uint_as_float(vs1[mt][b]);
-          const float w00 = p00 * fac0[b] * s0, w01 = p01 * fac1[b] * s0, w10 = p10 * fac0[b] * s1, w11 = p11 * fac1[b] * s1;
+          const uint64_t fac = f2_pack(fac0[b], fac1[b]);
+          float w00, w01, w10, w11;
+          f2_unpack(f2_mul(f2_mul(f2_pack(p00, p01), fac), f2_pack(s0, s0)), w00, w01);
+          f2_unpack(f2_mul(f2_mul(f2_pack(p10, p11), fac), f2_pack(s1, s1)), w10, w11);
           const uint32_t r0 = f16x2(w00, w01), r1 = f16x2(w10, w11);
           pf[0][b][0] = transpose8x8(r0);
           pf[0][b][1] = transpose8x8(r1);
