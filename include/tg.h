@@ -612,8 +612,9 @@ int tg_kv4_load(const tg_kv4_cache* cache, const int32_t* slots, int64_t rows, v
  *     l_c = head_temp[h] * ratio[r] * sm_scale * (q_h . k_c) + head_gain[h] * bias[c]
  *     out_h = sum_c softmax_c(l) v_c,   lse_h = log sum_c exp(l_c)
  * A key whose bias is -infinity is left out, whatever its row holds and whatever the gain.
- * A finite bias makes a finite logit: beyond +-2.3e38 (the largest float over log2 e) logits
- * count as that, so keys that all have the type's lowest value as bias share the weight.
+ * A finite bias makes a finite logit (the content term being finite): beyond +-2.3e38 (the largest
+ * float over log2 e) logits count as that, so keys that all have the type's lowest value as bias
+ * share the weight.
  * A request with no row left gets zeros and lse -infinity.
  *   q      device, dtype, request r's head h at q + r*ldq + h*head_dim
  *   tables device int32 [nreq][max_pages], lens device int32 [nreq] (as

@@ -49,7 +49,7 @@ __device__ __forceinline__ int64_t kv4_row(const Kv4Cache& c, int32_t slot, int 
 // order the reads of the old state before the writes of the new one, so the
 // state may be updated in place.  Bound by latency: the two barriers and the
 // dependent loads (length -> page -> slot).  Device time: one more row for 56 of 64
-// requests 6.6 us, 129828 rows for 1000 requests (pages of 16, 0.6 MB) 12.3 us.
+// requests 6.5 us, 129828 rows for 1000 requests (pages of 16, 0.6 MB) 12.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 constexpr int kTabMaxReq = 4096;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
   // A warp takes 32 neighbouring slots up to eight times in a row, as often as it takes to go
   // round once: one search for the first row's request, then short walks, and the page ids a
   // lane needs on their way together.  129828 slots of 1000 requests, 16 CTAs: eight times
-  // 12.0 us, twice 15.5; one slot for each of 1000 requests, where a walk passes as many
+  // 12.4 us, twice 15.5; one slot for each of 1000 requests, where a walk passes as many
   // requests as slots: 15.1 and 9.0.
   const int lane = threadIdx.x & 31;
   const int times = max(1, min(kTabTimes, (p.nslots + step - 1) / step));
@@ -270,9 +270,11 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const PageTablePara
 
 // ---------------------------------------------------------------------------
 // Rows in and out.  Four lanes share a group of 32 dimensions, eight dimensions
-// (one 16-byte load in bf16) each.  Bound by memory for many rows: 8256 rows of 8 heads
-// of 128, bf16, K and V: in 13.9 us (43 MB, 3.1 TB/s), in and out 29.9 us (121 MB with fp32
-// values out, 4.0 TB/s, 62 % of a copy's rate); by the launch for a decode step's.
+// (one 16-byte load in bf16) each.  8256 rows of 8 heads of 128, K and V, pages of 64: in 14.0 us
+// (bf16, 43 MB, 3.1 TB/s, 47 % of a copy's rate; fp32, 77 MB, 17.5 us, 67 %), out 13.4 (bf16)
+// and 17.4 (fp32); bf16 in and then fp32 out 30.1 us (121 MB, 61 %).  Bound by the instructions: 10.1 M
+// warp instructions in (bf16) and 11.9 M out (fp32), issued in 70 and 74 % of the
+// cycles, the logic pipe 64 % busy with both.  A decode step's rows are bound by the launch.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8]);

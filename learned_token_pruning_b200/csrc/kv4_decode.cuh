@@ -5,13 +5,12 @@
 // -infinity is left out altogether, whatever its row holds; a request without
 // keys gets zeros (lse -infinity).
 //
-// The cache is read once and the step is bound by memory: 2 (D/2 + D/16) bytes per
-// row and KV head, a third of bf16.  What stands in the way is the work per value,
-// so the products run on the tensor cores through the warp-level matrix
-// instruction (m16n8k16, fp16 in, fp32 out).  Its operands come from registers,
-// where the codes are widened with one conversion per two values; the wide
-// tcgen05 form would need them written back to shared memory first, and its
-// 128-row tiles have nothing to fill them with at 1 to 8 query heads.
+// The cache is read once: 2 (D/2 + D/16) bytes per row and KV head, a third of bf16, are the
+// floor.  What stands in the way is the work per value, so the products run on the
+// tensor cores through the warp-level matrix instruction (m16n8k16, fp16 in, fp32
+// out).  Its operands come from registers, where the codes are widened with one
+// conversion per two values.  The wide tcgen05 form, keys as its 128 rows and the codes
+// taken by it from shared memory as they are, has not been tried.
 //
 //   Keys and values are the A operand (16 keys or 16 dimensions x 16), the query
 //   heads and the weights the B operand (8 columns).  E2M1 codes are exact in
@@ -39,12 +38,15 @@
 // reruns are bit-identical.
 //
 // Measured (16 + 8 heads of 128, bf16 queries, both kernels): 131137 rows of one request, pages
-// of 128: 40.6 us, 152 MB, 3.7 TB/s (57 % of a copy's 6.55); pages of 16: 45.7; a ragged batch of
-// 33 requests of up to 8321 rows, pages of 16: 48.3; 2129 rows: 10.4.  About 25 us of the 40
-// are the stream itself, the same when the cache sits in L2: 18.5 M warp instructions at 0.47 a
-// cycle and scheduler, with the logic pipe that takes the codes apart 44 % busy and the matrix
-// pipe 21 %.  Finite logits and units for any finite bias and value scale cost 0.5 us of them.  The other 15 are latency: the plan, the first page ids and keys, a run's
-// whole tiles, the pieces and the second kernel.
+// of 128: 40.3 us, 152 MB, 3.8 TB/s (57 % of a copy's 6.55); pages of 16: 45.3; a ragged batch of
+// 33 requests of up to 8321 rows, pages of 16: 48.2; 2129 rows: 10.4; fp32 queries over 131137
+// rows, pages of 64: 48.2 (the weights and queries in two parts each: more matrix instructions and
+// registers, 8 warps).  From 131072 to 262144 rows 25.3 us are added, 25.1 where the tables
+// name 8 pages over and over, which L2 holds: the stream of 25 us is not bound by memory, though it
+// runs at 91 % of a copy's rate, but by the instructions.  There are 18.3 M warp instructions,
+// over the whole kernel 0.47 a cycle and scheduler, with the logic pipe that takes the codes apart
+// 44 % busy.  The other 15 us are latency: the plan, the first page ids and keys, a
+// run's whole tiles, the pieces and the second kernel.
 // Tried: tiles of 32 keys, 41 .. 52 us; 16-byte copies by every lane in place of the bulk
 // copies, 51.5 (pages of 16: 55.7 against 56.5 then), for the scales and biases alone 41.7 (pages
 // of 16: 43.6 against 45.2); two or three CTAs per SM, 42 .. 59; merging by a ticket
@@ -65,12 +67,13 @@ constexpr float kKv4Slack = 4.0f;   // a weight may exceed 1 by 2^4 before the r
 constexpr int kKv4WeightExp = 10;   // a weight times a scale that is one unit lands at 2^10: 2^15 at most in fp16
 // A unit is set 2^3 above the largest product of a weight and a scale.  More makes moves rarer and
 // rounds coarser: 131137 rows (16 + 8 heads), value scales that spread by 2^4 (one standard deviation)
-// and biases of 6 between rows, 2^3 43.2 us, 2^6 42.9; ordinary rows 40.5 with both.
+// and biases of 6 between rows, 2^3 43.4 us, 2^6 43.0; ordinary rows 40.3 with both.
 constexpr int kKv4Over = 3;
 constexpr int kKv4LeastUnit = 14;   // the smallest unit: its factor, 2^123, times a weight, 2^4 at most, is a float
 
 // Warps of one CTA (one CTA per SM): as many as registers hold.  bf16, 12 against 8: the ragged
-// batch 47.7 / 50.1 us, 64 requests of 200 rows 13.5 / 15.1, 131137 rows 40.2 / 39.9.  With 8 heads
+// batch 48.2 / 52.4 us, 64 requests of 200 rows 13.8 / 16.3, 131137 rows 40.3 / 41.4, 4 requests
+// of 32761 rows of 4 + 4 heads 22.3 / 21.4.  With 8 heads
 // a B operand, or two parts of queries and weights, a thread needs up to 248 registers.
 template <typename T, int HP>
 struct Kv4Cfg {
@@ -96,7 +99,7 @@ struct Kv4DecodeParams {
 };
 
 // Cost a CTA takes before another one joins (3 at least: see kv4_tiles_before).  4 against 12:
-// 2129 rows 10.1 / 10.6 us, fp32 queries over 5 requests of up to 997 rows 9.5 / 9.9.
+// 2129 rows 10.4 / 11.0 us, fp32 queries over 5 requests of up to 997 rows 10.0 / 10.5.
 constexpr int kKv4MinCost = 4;
 
 // one piece of a (request, head): group rows of D sums, then the maxima, then the weight sums

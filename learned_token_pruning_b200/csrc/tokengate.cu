@@ -415,7 +415,7 @@ bool select_cluster16_ok() {
 }
 
 // CTAs of the page tables' cluster: 16 (a non-portable size) where one can be resident, else 8;
-// checked once per device.  129828 slots of 1000 requests take 12.0 us with 16, 18.4 with 8,
+// checked once per device.  129828 slots of 1000 requests take 12.4 us with 16, 18.4 with 8,
 // 31.2 with 4; one slot of one request 4.7, 4.6 and 4.6.
 unsigned page_table_ctas() {
   static std::mutex mu;
@@ -1809,8 +1809,8 @@ int qk_rope_blocks() { return 2 * sm_count(); }
 // first: rounds of items times a part's passes and its table of angles, which takes as
 // long as about a pass and a half.  Whole rows in rounds of 16 warps an SM leave the last round
 // idle, parts repeat the angles: 16 + 8 heads of 128, bf16, whole against cut, backward of
-// 592 rows 12.1 / 10.3 us, 3000 rows 22.6 / 22.0; parts chosen with half that price for the
-// table (forward of 8256 rows in two parts) 20.3 us against 18.6 whole.
+// 592 rows 10.0 / 9.6 us, 3000 rows 22.6 / 21.7; parts chosen with half that price for the
+// table (forward of 8256 rows in two parts) 22.4 us against 21.1 whole.
 void qk_rope_cut(tg::QkRopeParams& p, int passes, int most) {
   p.split = 1;
   p.per = passes;
@@ -2071,10 +2071,11 @@ int kv4_rows(const char* what, bool load, const tg_kv4_cache* cache, const void*
   p.slots = slots;
   p.rows = rows;
   // items of eight K or V values: a block takes 256 of a row, or as many whole rows, several
-  // times over where that fills the GPU.  8256 rows x 8 heads of 128, bf16: the loads of
-  // four rows under way together, 13.9 us into the cache, of one 18.1; out of it (fp32)
-  // two 17.9 us, one 18.9, four 22.7.  33 rows x 2 heads of 64, in and out: one
-  // 3.4 us, four 7.0
+  // times over where that fills the GPU.  8256 rows x 8 heads of 128: the loads of four rows
+  // under way together, 14.0 us into the cache (bf16), of one 18.0; out of it two 13.4 us
+  // (bf16) and 17.4 (fp32), one 17.4 and 19.9, four 12.3 and 16.5, but 2064 rows two 4.6 and
+  // 5.4, four 5.3 and 6.1, and right behind the rows' way in (bf16, then fp32 out) two 30.1
+  // for both, four 30.7.  33 rows x 2 heads of 64, in and out: one 3.4 us, four 7.0
   const int64_t per_row = width / 4, per_block = per_row < 256 ? 256 / per_row : 1, chunks = (per_row + 255) / 256;
   if (chunks > 65535) return fail(TG_ERR_UNSUPPORTED, "hkv * head_dim is too large");
   auto run = [&](auto several, auto one) {
@@ -2119,8 +2120,8 @@ int launch_kv4_decode_hp(const tg::Kv4DecodeParams& p, cudaStream_t st) {
 }
 
 // The fewest head columns that hold the group, so that one B operand serves as many scale
-// groups as it can: a group of 2 over 131137 rows (pages of 128) with 2 columns 40.2 us, 4
-// 41.4, 8 42.6; the ragged batch 47.7, 48.5, 52.2; a group of 1 the same to 5 % either way.
+// groups as it can: a group of 2 over 131137 rows (pages of 128) with 2 columns 40.3 us, 4
+// 42.1, 8 45.9; the ragged batch 48.2, 50.2, 56.5; a group of 1 the same to 5 % either way.
 // Head dim 64 has two scale groups, which 4 columns already serve.
 template <typename T, int D>
 int launch_kv4_decode(const tg::Kv4DecodeParams& p, cudaStream_t st) {
