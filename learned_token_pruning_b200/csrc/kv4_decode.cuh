@@ -40,7 +40,7 @@
 // Measured (16 + 8 heads of 128, bf16 queries, both kernels): 131137 rows of one request, pages
 // of 128: 40.3 us, 152 MB, 3.8 TB/s (57 % of a copy's 6.55); pages of 16: 45.3; a ragged batch of
 // 33 requests of up to 8321 rows, pages of 16: 48.2; 2129 rows: 10.4; fp32 queries over 131137
-// rows, pages of 64: 48.2 (the weights and queries in two parts each: more matrix instructions and
+// rows, pages of 64: 49.5 (the weights and queries in two parts each: more matrix instructions and
 // registers, 8 warps).  From 131072 to 262144 rows 25.3 us are added, 25.1 where the tables
 // name 8 pages over and over, which L2 holds: the stream of 25 us is not bound by memory, though it
 // runs at 91 % of a copy's rate, but by the instructions.  There are 18.3 M warp instructions,
@@ -728,7 +728,12 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
       }
       const float use0 = m0 == -INFINITY ? 0.0f : m0, use1 = m1 == -INFINITY ? 0.0f : m1;
 
-      // ---- weights, and their products with the values
+      // ---- weights, and their products with the values.  The matrix unit cuts its fp32 sums where an
+      // addition rounds them, and the cuts of a long run add up: with fp32 queries a tile is summed
+      // on its own and added to the run's.  Relative error of 131137 rows 4.8e-7, without it 1.8e-6
+      // (and growing with the rows: 76 million rows of one KV head 3.6e-4); 49.5 us, without it 48.2.
+      // With bf16 queries the cuts stay below 2^-12 up to some 150 million rows.
+      float tile_o[kSplit ? NG : 1][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float p00 = kv4_ex2(x[mt][0] - use0), p01 = kv4_ex2(x[mt][1] - use1);
@@ -778,10 +783,22 @@ __global__ void __launch_bounds__(32 * Kv4Cfg<T, HP>::kWarps, 1) k_kv4_decode(co
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int v = 0; v < (kSplit ? 2 : 1); ++v)
-                mma_f16(o[2 * w + i][j], loab[2 * i + j], hiab[2 * i + j], locd[2 * i + j], hicd[2 * i + j],
-                        pf[v][(2 * w + i) / SL][0], pf[v][(2 * w + i) / SL][1]);
+              for (int v = 0; v < (kSplit ? 2 : 1); ++v) {
+                const int g = 2 * w + i, b = g / SL;
+                const uint32_t a0 = loab[2 * i + j], a1 = hiab[2 * i + j], a2 = locd[2 * i + j], a3 = hicd[2 * i + j];
+                if constexpr (!kSplit) mma_f16(o[g][j], a0, a1, a2, a3, pf[v][b][0], pf[v][b][1]);
+                else if (mt + v == 0) mma_f16_zero(tile_o[g][j], a0, a1, a2, a3, pf[v][b][0], pf[v][b][1]);
+                else mma_f16(tile_o[g][j], a0, a1, a2, a3, pf[v][b][0], pf[v][b][1]);
+              }
         }
+      }
+      if constexpr (kSplit) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[g][j][c] += tile_o[g][j][c];
       }
       __syncwarp();  // every lane has read the values
       if (i + 1 < left) load_values();
